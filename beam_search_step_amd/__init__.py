@@ -502,6 +502,10 @@ class PagedKV:
             d = make_kv_pool(d)
         bs_kv_paged_reorder(self.h, d, gen_len)
 
+    def reorder_quant(self, caches, gen_len: int):
+        """The reorder of layers held in 8 bits (QuantCache): data and scales."""
+        bs_kvq_reorder(self.h, caches, gen_len)
+
     def status(self):
         return bs_kv_paged_status(self.h, self.search.B)
 
@@ -568,3 +572,7 @@ class Verifier:
         bs_verify_ex(self.h, logits, proposals, top_k, min_block, self.accept_len, self.argmax,
                      rk)
         return (self.accept_len, self.argmax, rk) if rank else (self.accept_len, self.argmax)
+
+
+from .attn import (BlockMap, CacheAttention, CrossAttention, QuantCache,  # noqa: E402,F401
+                   attn_functions, attn_library, bs_kvq_reorder)

@@ -90,17 +90,6 @@ struct bs_state {
   bs_kv_paged* caches;  // every paged cache created on the handle (linked)
 };
 
-struct bs_kv_paged {
-  bs_state* h;          // null once the handle is destroyed (the cache is orphaned)
-  bs_kv_paged* next;    // the handle's next cache
-  hipStream_t stream;   // the handle's stream
-  int bs, bpi, mb;
-  int last_t;   // the step last reordered (0: none since the reset)
-  int table_t;  // the step whose table update has run (0: none since the reset)
-  void* block;
-  PagedDev pg;
-};
-
 struct bs_verify_state {
   hipStream_t stream;
   int device;
@@ -784,6 +773,9 @@ int bs_kv_paged_create(bs_state* h, int32_t block_size, int32_t blocks_per_item,
   if (!p) return BS_ENOMEM;
   p->h = h;
   p->stream = h->stream;
+  p->device = h->device;
+  p->rows = h->B * h->W;
+  p->blocks = h->B * blocks_per_item;
   p->bs = block_size;
   p->bpi = blocks_per_item;
   p->mb = mb;

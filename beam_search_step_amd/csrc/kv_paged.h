@@ -3,6 +3,8 @@
 // The paged KV cache with copy on write: K6, K7.
 #pragma once
 
+#include "paged_dev.h"
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -11,16 +13,6 @@ namespace {
 
 constexpr int kPagedMaxBlocks = 4096;  // blocks per item (LDS reference counts)
 constexpr int kPagedMaxTable = 2048;   // W * max_blocks (LDS table copies)
-
-struct PagedDev {
-  int* table;     // [B*W][mb] global block ids, -1 = none
-  int* refc;      // [B*bpi] live-row references of each block
-  int* freel;     // [B][bpi] stack of free global block ids
-  int* nfree;     // [B]
-  int* overflow;  // [1]
-  int* cpy;       // [B*W][3] copy list of the step: source block, destination block, positions
-  int* ncpy;      // [2] entries of the list, by step parity
-};
 
 struct K6Args {
   PagedDev pg;
