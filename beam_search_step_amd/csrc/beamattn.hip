@@ -9,6 +9,7 @@
 //   q3_scales   (kvq.h)          scales of the blocks that a reorder copied
 //   a1_cache    (cache_attn.h)   attention over that cache
 //   a2_cross    (cross_attn.h)   attention to an encoder's states
+//   a3_tile     (cross_tile.h)   the same for many rows, keys shared through LDS
 //   a_combine   (attn_common.h)  joins the sums of keys that were split
 
 #include <hip/hip_runtime.h>
@@ -32,6 +33,7 @@
 #include "kvq.h"
 #include "cache_attn.h"
 #include "cross_attn.h"
+#include "cross_tile.h"
 
 // ===========================================================================
 // host runtime
@@ -249,6 +251,14 @@ void launch_cross(const CrossArgs& a, int dtype, int nm, dim3 grid, hipStream_t 
     else if (dp == 128) launch_cross_n<128, float>(a, nm, grid, s);
     else launch_cross_n<256, float>(a, nm, grid, s);
   }
+}
+
+constexpr int64_t kTileCols = 64;  // more columns than this share keys through LDS
+void launch_tile(const CrossArgs& a, dim3 grid, hipStream_t s) {
+  const int dp = pad_dim(a.q.D);
+  if (dp == 64) hipLaunchKernelGGL(a3_tile<64>, grid, dim3(kAttnThreads), 0, s, a);
+  else if (dp == 128) hipLaunchKernelGGL(a3_tile<128>, grid, dim3(kAttnThreads), 0, s, a);
+  else hipLaunchKernelGGL(a3_tile<256>, grid, dim3(kAttnThreads), 0, s, a);
 }
 
 // one allocation: the maxima and sums, then the partial sums
@@ -593,9 +603,12 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   a.mask_stride = mask_stride;
   const int64_t cols = (int64_t)n_rows * a.q.group;
   const int nm = column_tiles(cols, cross_tiles_most(pad_dim(c.head_dim), c.dtype));
-  a.groups = (int)((cols + 16 * nm - 1) / (16 * nm));
+  const bool tile = c.dtype == BS_BF16 && cols > kTileCols;
+  const int per = tile ? 128 : 16 * nm;
+  a.pairs = c.batch * c.kv_heads;
+  a.groups = (int)((cols + per - 1) / per);
   const int64_t units = (int64_t)c.batch * n_rows * c.heads;
-  const int64_t wg = (int64_t)c.batch * c.kv_heads * a.groups;
+  const int64_t wg = (int64_t)(tile ? (a.pairs + 7) / 8 * 8 : a.pairs) * a.groups;
   a.splits = choose_splits(wg, n_keys, kMaxSplits);
   if (a.splits > 1 && units * a.splits > h->units) {
     a.splits = (int)(h->units / units);
@@ -605,7 +618,11 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   a.q.ns = a.splits;
   a.q.pml = h->pml;
   a.q.pacc = h->pacc;
-  launch_cross(a, c.dtype, nm, dim3((unsigned)(wg * a.splits)), h->stream);
+  const dim3 grid((unsigned)(wg * a.splits));
+  if (tile)
+    launch_tile(a, grid, h->stream);
+  else
+    launch_cross(a, c.dtype, nm, grid, h->stream);
   int rc = launch_status();
   if (rc == BS_OK && a.splits > 1) rc = launch_combine(a.q, units, c.dtype, h->stream);
   return rc;

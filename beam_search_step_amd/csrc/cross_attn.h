@@ -17,6 +17,7 @@ struct CrossArgs {
   const uint8_t* mask;                // [B][mask_stride] or null
   int64_t mask_stride;
   int splits, groups;
+  int pairs;                          // items * kv heads
 };
 
 // The keys n0 .. n0 + 31 that an item sees, as bits.

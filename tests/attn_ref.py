@@ -6,7 +6,8 @@ Tolerances count roundings. With u = 2^-23 for a rounding or a truncation of a
 most (T D + 4) u times the sum S of its products' magnitudes, so a probability's
 relative error is below 2 (T D + 4) u S (numerator and denominator); the sum over
 n keys and its joins add (n + 64) u, the two-term probabilities of bf16 calls
-2^-15, all of them relative to A = sum p |v|. The output's own rounding adds
+2^-15 (where one bf16 term is used, with a sum of the same rounded terms: 2^-8 in
+each of the two, 2^-7), all of them relative to A = sum p |v|. The output's own rounding adds
 eps / 2 of its type relative to the value.
 
 These are relative errors, and 32-bit numbers end at 2^-126: a probability below
@@ -100,7 +101,7 @@ def write(values, scale, x, slots):
         i += run
 
 
-def attend(q, k, v, seen, scale, dtype, terms):
+def attend(q, k, v, seen, scale, dtype, terms, one_term=False):
     """(values, tolerance) of queries q [m, D] over keys k, v [n, D] with seen [m, n]
     (bool), all float64."""
     m, d = q.shape
@@ -119,6 +120,7 @@ def attend(q, k, v, seen, scale, dtype, terms):
         if bool(torch.isnan(v).any()) else p @ v
     a = p @ torch.nan_to_num(v).abs()
     half, extra = (2.0 ** -8, 2.0 ** -15) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -23)
+    extra = 2.0 ** -7 if one_term else extra
     rel = 2 * (terms * d + 4) * U * mag + (k.shape[0] + 64) * U + extra
     low = k.shape[0] * 2.0 ** -124 * (float(torch.nan_to_num(v, posinf=0, neginf=0).abs().max()) + 1)
     return o, half * o.abs() + rel * a * (1 + half) + low
@@ -160,6 +162,7 @@ def cache_attention(q, kv, vv, table, lens, ptable, plens, q_len, rows, scale, d
 
 
 def cross_attention(q, k, v, lens, mask, scale, dtype):
+    # bf16 calls of more than 64 columns (rows * grouped heads) round probabilities to bf16
     """(values, tolerance) for q [B, R, Hq, D], k, v [B, S, Hkv, D] in float64."""
     b, rows, hq, d = q.shape
     hk = k.shape[2]
@@ -175,7 +178,8 @@ def cross_attention(q, k, v, lens, mask, scale, dtype):
             sl = slice(h * grp, (h + 1) * grp)
             x = q[i, :, sl].reshape(-1, d)
             seen = torch.ones(x.shape[0], at.numel(), dtype=torch.bool)
-            y, t = attend(x, k[i, at, h], v[i, at, h], seen, scale, dtype, 1)
+            y, t = attend(x, k[i, at, h], v[i, at, h], seen, scale, dtype, 1,
+                          dtype == "bf16" and rows * grp > 64)
             o[i, :, sl], tol[i, :, sl] = y.view(rows, grp, d), t.view(rows, grp, d)
     return o, tol
 
