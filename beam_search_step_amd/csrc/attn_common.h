@@ -109,10 +109,10 @@ struct Softmax {
 };
 
 // The sums of a workgroup's waves, joined in LDS in wave order, then the
-// result or the workgroup's partial.
+// result or the workgroup's partial. One barrier: the waves write side by side.
 template <int DP, int NM>
 struct JoinLds {
-  float acc[16 * NM][DP + 4];
+  float acc[kAttnWaves][16 * NM][DP + 4];
   float m[kAttnWaves][16 * NM], l[kAttnWaves][16 * NM];
 };
 
@@ -146,35 +146,17 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
       lds.l[wave][16 * i + c] = l;
     }
   }
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < NM; ++i) {
-    const int col = 16 * i + c;
-    float M = lds.m[0][col];
+  for (int i = 0; i < NM; ++i)
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) M = fmaxf(M, lds.m[w][col]);
-    const float f = sm.m[i] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(sm.m[i] - M);
+    for (int r = 0; r < 4; ++r) {
+      float* p = &lds.acc[wave][16 * i + c][VD * (4 * g + r)];
 #pragma unroll
-    for (int j = 0; j < VD; ++j) acc[i][j] *= f;
-  }
-#pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) {
-    if (wave == w) {
-#pragma unroll
-      for (int i = 0; i < NM; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float* p = &lds.acc[16 * i + c][VD * (4 * g + r)];
-#pragma unroll
-          for (int j = 0; j < VD; j += 4) {
-            f32x4 v = {acc[i][j][r], acc[i][j + 1][r], acc[i][j + 2][r], acc[i][j + 3][r]};
-            if (w > 0) v += *reinterpret_cast<f32x4*>(p + j);
-            *reinterpret_cast<f32x4*>(p + j) = v;
-          }
-        }
+      for (int j = 0; j < VD; j += 4)
+        *reinterpret_cast<f32x4*>(p + j) =
+            f32x4{acc[i][j][r], acc[i][j + 1][r], acc[i][j + 2][r], acc[i][j + 3][r]};
     }
-    __syncthreads();
-  }
+  __syncthreads();
   for (int idx = tid; idx < 16 * NM * (DP / 4); idx += kAttnThreads) {
     const int x = idx / (DP / 4), d = (idx - x * (DP / 4)) * 4;
     const int col = col0 + x;
@@ -183,17 +165,19 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
 #pragma unroll
     for (int w = 1; w < kAttnWaves; ++w) M = fmaxf(M, lds.m[w][x]);
     float L = 0.0f;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w)
-      L += lds.m[w][x] == -kInf ? 0.0f : lds.l[w][x] * __builtin_amdgcn_exp2f(lds.m[w][x] - M);
-    f32x4 v = *reinterpret_cast<f32x4*>(&lds.acc[x][d]);
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float mw = lds.m[w][x];
+      const float f = mw == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mw - M);
+      L += f * lds.l[w][x];
+      v += f * *reinterpret_cast<f32x4*>(&lds.acc[w][x][d]);
+    }
     const int qr = fast_div(a.by_group, col);
     const int64_t u = (row0 + qr) * a.heads + head0 + (col - qr * a.group);
     if (a.ns == 1) {
-      const bool none = M == -kInf;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = none ? 0.0f : v[k] / L;
-      store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v);
+      const float f = M == -kInf ? 0.0f : __builtin_amdgcn_rcpf(L);
+      store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v * f);
     } else {
       if (d == 0) {
         float* p = a.pml + (u * a.ns + split) * 2;
@@ -206,41 +190,52 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
 }
 
 // Joins the partials of one query and head: out = sum_s 2^(m_s - M) acc_s /
-// sum_s 2^(m_s - M) l_s, the splits that saw nothing left out. One wave each;
-// lane s holds the weight of split s.
+// sum_s 2^(m_s - M) l_s, over those that saw something. LPU lanes take one query
+// and head, four values each, eight partials in flight.
 struct CombineArgs {
   const float* pacc;
   const float* pml;
   void* out;
-  int64_t units;
+  int64_t units;   // query rows * heads
   int ns, D;
 };
-template <typename TO>
+template <typename TO, int LPU>
 __global__ __launch_bounds__(kAttnThreads) void a_combine(CombineArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t u = (int64_t)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
-  if (u >= a.units) return;
-  float m = -kInf, l = 0.0f;
-  if (lane < a.ns) {
-    const float* p = a.pml + (u * a.ns + lane) * 2;
-    m = p[0];
-    l = p[1];
-  }
-  const float M = wave_max_f(m);
-  const float w = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - M);
-  const float L = wave_sum_f(m == -kInf ? 0.0f : w * l);
-  const uint64_t seen = __ballot(m != -kInf);
-  for (int d = lane * 4; d < a.D; d += 256) {
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < a.ns; ++s) {
-      if (!((seen >> s) & 1)) continue;
-      const float ws = as_f(__builtin_amdgcn_readlane((int)as_u(w), s));
-      v += ws * *reinterpret_cast<const f32x4*>(a.pacc + (u * a.ns + s) * a.D + d);
-    }
+  const int tid = threadIdx.x, sub = tid / LPU, d = (tid - sub * LPU) * 4;
+  const int64_t u = (int64_t)blockIdx.x * (kAttnThreads / LPU) + sub;
+  if (u >= a.units || d >= a.D) return;
+  const float* ml = a.pml + u * a.ns * 2;
+  const float* pa = a.pacc + u * a.ns * a.D + d;
+  float M = -kInf, L = 0.0f;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < a.ns; s0 += 8) {
+    f32x4 x[8];
+    f32x2 y[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = seen ? v[k] / L : 0.0f;
-    store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v);
+    for (int k = 0; k < 8; ++k) {
+      const int s = min(s0 + k, a.ns - 1);
+      y[k] = *reinterpret_cast<const f32x2*>(ml + s * 2);
+      x[k] = *reinterpret_cast<const f32x4*>(pa + (int64_t)s * a.D);
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, y[k].x);
+    if (top == -kInf) continue;
+    const float f = M == -kInf ? 0.0f : __builtin_amdgcn_exp2f(M - top);
+    L *= f;
+    v *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // a split that saw nothing left its sums unwritten
+      if (s0 + k >= a.ns || y[k].x == -kInf) continue;
+      const float w = __builtin_amdgcn_exp2f(y[k].x - top);
+      L += w * y[k].y;
+      v += w * x[k];
+    }
+    M = top;
   }
+  const float f = M == -kInf ? 0.0f : __builtin_amdgcn_rcpf(L);
+  store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, M == -kInf ? f32x4{0, 0, 0, 0} : v * f);
 }
 
 // ---------------------------------------------------------------------------

@@ -188,11 +188,18 @@ int launch_combine(const QueryArgs& q, int64_t units, int dtype, hipStream_t s) 
   c.units = units;
   c.ns = q.ns;
   c.D = q.D;
-  const dim3 grid((unsigned)((units + kAttnWaves - 1) / kAttnWaves));
-  if (dtype == BS_F32)
-    hipLaunchKernelGGL(a_combine<float>, grid, dim3(kAttnThreads), 0, s, c);
-  else
-    hipLaunchKernelGGL(a_combine<uint16_t>, grid, dim3(kAttnThreads), 0, s, c);
+  const int lpu = q.D <= 64 ? 16 : q.D <= 128 ? 32 : 64;  // four values a lane
+  const int per = kAttnThreads / lpu;
+  const dim3 grid((unsigned)((units + per - 1) / per)), blk(kAttnThreads);
+  if (dtype == BS_F32) {
+    if (lpu == 16) hipLaunchKernelGGL((a_combine<float, 16>), grid, blk, 0, s, c);
+    else if (lpu == 32) hipLaunchKernelGGL((a_combine<float, 32>), grid, blk, 0, s, c);
+    else hipLaunchKernelGGL((a_combine<float, 64>), grid, blk, 0, s, c);
+  } else {
+    if (lpu == 16) hipLaunchKernelGGL((a_combine<uint16_t, 16>), grid, blk, 0, s, c);
+    else if (lpu == 32) hipLaunchKernelGGL((a_combine<uint16_t, 32>), grid, blk, 0, s, c);
+    else hipLaunchKernelGGL((a_combine<uint16_t, 64>), grid, blk, 0, s, c);
+  }
   return launch_status();
 }
 

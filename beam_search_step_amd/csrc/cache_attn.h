@@ -188,7 +188,6 @@ template <int DP, int NM, int NT, bool UNI>
 __global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
   using TO = typename std::conditional<NT == 1, uint16_t, float>::type;
   constexpr int NP = NT == 1 ? 2 : 3;
-  constexpr bool AHEAD = DP < 256 && (UNI || DP < 128);  // registers for a second step
   __shared__ JoinLds<DP, NM> lds;
   const int lane = threadIdx.x & 63, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -230,12 +229,11 @@ __global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
 
   int n0 = begin + wave * kStep;
   if (n0 < end) {
-    RawKv<DP> cur, next;
+    RawKv<DP> cur;
     load_step<DP, UNI>(a, trow, len, n0, h, cur);
     while (true) {
       const int n1 = n0 + kAttnWaves * kStep;
       const bool more = n1 < end;
-      if (AHEAD && more) load_step<DP, UNI>(a, trow, len, n1, h, next);
       if (cur.bm) {
         int lim[NM];
 #pragma unroll
@@ -246,10 +244,7 @@ __global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
             s.back && n0 + kStep > open, lim);
       }
       if (!more) break;
-      if (AHEAD)
-        cur = next;
-      else
-        load_step<DP, UNI>(a, trow, len, n1, h, cur);
+      load_step<DP, UNI>(a, trow, len, n1, h, cur);
       n0 = n1;
     }
   }

@@ -221,7 +221,6 @@ __device__ __forceinline__ void step_f32(const QueryF32<DP, NM>& q, Softmax<NM>&
 template <int DP, int NM, typename T>
 __global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr bool AHEAD = DP < 256 && DP * NM <= (F32 ? 128 : 256);
   __shared__ JoinLds<DP, NM> lds;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int idx = blockIdx.x;
@@ -253,12 +252,11 @@ __global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
 
   int n0 = begin + wave * kStep;
   if (n0 < end) {
-    typename std::conditional<F32, RawF32<DP>, RawBf16<DP>>::type cur, next;
+    typename std::conditional<F32, RawF32<DP>, RawBf16<DP>>::type cur;
     load_step<DP>(a, kb, vb, mrow, len, n0, cur);
     while (true) {
       const int n1 = n0 + kAttnWaves * kStep;
       const bool more = n1 < end;
-      if (AHEAD && more) load_step<DP>(a, kb, vb, mrow, len, n1, next);
       if (cur.bm) {
         if constexpr (F32) {
           step_f32<DP, NM>(q, sm, acc, cur, a.q.c, a.q.D);
@@ -270,10 +268,7 @@ __global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
         }
       }
       if (!more) break;
-      if (AHEAD)
-        cur = next;
-      else
-        load_step<DP>(a, kb, vb, mrow, len, n1, cur);
+      load_step<DP>(a, kb, vb, mrow, len, n1, cur);
       n0 = n1;
     }
   }
