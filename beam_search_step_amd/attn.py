@@ -84,29 +84,45 @@ def attn_functions() -> list:
     return sorted(set(re.findall(r"\b(bs_[a-z_]+)\s*\(", text)))
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported at the first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _torch_dtypes():
-    import torch
+    torch = _t()
     return {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
 def _need(t, what: str, device, dtype, shape=None):
     """A tensor on the device, of the type and, when a shape is given, contiguous and of it."""
+    if t.device == device and t.dtype is dtype and (
+            shape is None or (t.shape == shape and t.is_contiguous())):
+        return
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
-        raise ValueError(f"{what}: a contiguous tensor of shape {list(shape)} is needed, not "
-                         f"{list(t.shape)}")
+    raise ValueError(f"{what}: a contiguous tensor of shape {list(shape)} is needed, not "
+                     f"{list(t.shape)}")
 
 
 def _head_rows(t, what: str, lead: tuple, heads: int, dim: int) -> int:
     """Elements between the rows of a tensor [*lead, heads, dim] whose rows are
     contiguous and evenly spaced."""
-    if tuple(t.shape) != (*lead, heads, dim):
+    if t.shape != (*lead, heads, dim):
         raise ValueError(f"{what}: shape {list(t.shape)}, expected {[*lead, heads, dim]}")
+    if t.is_contiguous():
+        return heads * dim
     st = t.stride()
-    if st[-1] != 1 or (heads > 1 and st[-2] != dim):
+    if (dim > 1 and st[-1] != 1) or (heads > 1 and st[-2] != dim):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     n = [(s, k) for s, k in zip(lead, st) if s > 1]
     for (_, a), (s, b) in zip(n, n[1:]):
@@ -115,39 +131,39 @@ def _head_rows(t, what: str, lead: tuple, heads: int, dim: int) -> int:
     return n[-1][1] if n else heads * dim
 
 
-def _on(device):
-    """The device's context where it is not the current one."""
-    import contextlib
-    import torch
+def _on_device(device, stream, fn, *args):
+    """fn(raw stream, *args) with the device as the current one, on the given stream
+    or the device's current stream."""
+    torch = _t()
+    if stream is not None:
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _raw_stream(stream, device) -> Optional[int]:
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+        return fn(raw, *args)
+    with torch.cuda.device(device):
+        return fn(raw, *args)
 
 
 def _gpu_device(stream):
-    import torch
+    torch = _t()
     return stream.device if stream is not None else torch.device("cuda", torch.cuda.current_device())
 
 
 def _table_arg(table, rows: int, device):
     """(address, entries per row) of a block table: a tensor, or a PagedKV's own."""
-    import torch
     if isinstance(table, _bs.PagedKV):
         if table.search.B * table.search.W != rows:
             raise ValueError(f"table: {table.search.B * table.search.W} rows, {rows} needed")
         if table.search.device != device:
             raise ValueError(f"table: on {table.search.device}, expected {device}")
         return table._addr, table.max_blocks
-    _need(table, "table", device, torch.int32)
-    if table.dim() != 2 or table.shape[0] != rows or not table.is_contiguous():
+    _need(table, "table", device, _t().int32)
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != rows or not table.is_contiguous():
         raise ValueError(f"table: a contiguous tensor [{rows}, entries] is needed, not "
-                         f"{list(table.shape)}")
-    return table.data_ptr(), table.shape[1]
+                         f"{list(shape)}")
+    return table.data_ptr(), shape[1]
 
 
 class BlockMap:
@@ -161,7 +177,7 @@ class BlockMap:
     """
 
     def __init__(self, n, block_size, max_blocks, max_tokens, stream=None):
-        import torch
+        torch = _t()
         self.n, self.block_size, self.max_blocks, self.max_tokens = n, block_size, max_blocks, max_tokens
         if not (1 <= n <= 65535 and block_size >= 1 and max_blocks >= 1 and max_tokens >= 0
                 and block_size * max_blocks < 2 ** 31 and max_tokens < 2 ** 31):
@@ -173,10 +189,12 @@ class BlockMap:
         self.cu = torch.empty(n + 1, **kw)
         self.slots = torch.empty(max_tokens, **kw)
         self.used = torch.empty(1, **kw)
+        self._cu, self._used = self.cu.data_ptr(), self.used.data_ptr()
+        self._slots = self.slots.data_ptr() or None
         self._table = None
 
     def __call__(self, lens, free_blocks=None, starts=None, table=None):
-        import torch
+        torch = _t()
         i32, dev = torch.int32, self.device
         _need(lens, "lens", dev, i32, (self.n,))
         if starts is not None:
@@ -198,13 +216,12 @@ class BlockMap:
         at, width = _table_arg(table, self.n, dev)
         if width != self.max_blocks:
             raise ValueError(f"table: {width} entries per row, expected {self.max_blocks}")
-        with _on(dev):
-            # an empty list is a list still: any address will do
-            free = None if free_blocks is None else free_blocks.data_ptr() or self.used.data_ptr()
-            _bs._check(self._fn(_raw_stream(self.stream, dev), self.n, self.block_size,
-                                self.max_blocks, _bs._ptr(starts), lens.data_ptr(), free, n_free,
-                                at, self.cu.data_ptr(), self.slots.data_ptr() or None,
-                                self.max_tokens, self.used.data_ptr()), "bs_map_blocks")
+        # an empty list is a list still: any address will do
+        free = None if free_blocks is None else free_blocks.data_ptr() or self._used
+        _bs._check(_on_device(dev, self.stream, self._fn, self.n, self.block_size,
+                              self.max_blocks, _bs._ptr(starts), lens.data_ptr(), free, n_free,
+                              at, self._cu, self._slots, self.max_tokens, self._used),
+                   "bs_map_blocks")
         return table, self.slots, self.cu, self.used
 
 
@@ -219,7 +236,7 @@ class QuantCache:
     """
 
     def __init__(self, k, v, k_scale, v_scale, stream=None):
-        import torch
+        torch = _t()
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
             raise ValueError("k, v: two pools [n_blocks, block_size, kv_heads, head_dim] of one "
                              "shape, type and strides are needed")
@@ -243,11 +260,11 @@ class QuantCache:
                                 v_scale.data_ptr(), n, bs, h, d, block, pos)
         self._ref = ctypes.addressof(self.desc)
         self._dtypes = _torch_dtypes()
-        self._lib = attn_library()
+        self._write, self._read = attn_library().bs_kvq_write, attn_library().bs_kvq_read
 
     @classmethod
     def empty(cls, n_blocks, block_size, kv_heads, head_dim, device=None, stream=None):
-        import torch
+        torch = _t()
         kw = dict(device=device if device is not None else _gpu_device(stream))
         pools = [torch.zeros((n_blocks, block_size, kv_heads, head_dim), dtype=torch.uint8, **kw)
                  for _ in range(2)]
@@ -255,36 +272,37 @@ class QuantCache:
         return cls(*pools, *scales, stream=stream)
 
     def write(self, k, v, slots) -> None:
-        import torch
+        torch = _t()
         n = k.shape[0]
-        dt = self._dtypes["f32"] if k.dtype == self._dtypes["f32"] else self._dtypes["bf16"]
-        for t, what in ((k, "k"), (v, "v")):
-            _need(t, what, self.device, dt)
+        f32 = k.dtype is torch.float32
+        dt = torch.float32 if f32 else torch.bfloat16
+        _need(k, "k", self.device, dt)
+        _need(v, "v", self.device, dt)
         stride = _head_rows(k, "k", (n,), self.heads, self.head_dim)
         if _head_rows(v, "v", (n,), self.heads, self.head_dim) != stride:
             raise ValueError("k, v: rows must be equally spaced")
         _need(slots, "slots", self.device, torch.int32)
-        if slots.dim() != 1 or slots.numel() < n or not slots.is_contiguous():
-            raise ValueError(f"slots: a contiguous list of {n} is needed")
-        with _on(self.device):
-            _bs._check(self._lib.bs_kvq_write(
-                _raw_stream(self.stream, self.device), self._ref,
-                _bs.BS_F32 if dt == torch.float32 else _bs.BS_BF16, k.data_ptr(), v.data_ptr(),
-                stride, slots.data_ptr(), n), "bs_kvq_write")
+        if slots.dim() != 1 or slots.shape[0] < n or not slots.is_contiguous():
+            raise ValueError(f"slots: a contiguous list of at least {n} is needed")
+        _bs._check(_on_device(self.device, self.stream, self._write, self._ref,
+                              _bs.BS_F32 if f32 else _bs.BS_BF16, k.data_ptr(), v.data_ptr(),
+                              stride, slots.data_ptr(), n), "bs_kvq_write")
 
     def read(self, slots, dtype="f32"):
-        import torch
+        torch = _t()
         _need(slots, "slots", self.device, torch.int32)
         if slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: a contiguous list is needed")
-        n = slots.numel()
-        shape = (n, self.heads, self.head_dim)
-        with _on(self.device), torch.cuda.stream(self.stream):
-            k = torch.empty(shape, dtype=self._dtypes[dtype], device=self.device)
-            v = torch.empty_like(k)
-            _bs._check(self._lib.bs_kvq_read(
-                _raw_stream(self.stream, self.device), self._ref, _bs.DTYPES[dtype],
-                slots.data_ptr(), n, k.data_ptr(), v.data_ptr()), "bs_kvq_read")
+        n = slots.shape[0]
+        shape = (2, n, self.heads, self.head_dim)
+        if self.stream is None:
+            kv = torch.empty(shape, dtype=self._dtypes[dtype], device=self.device)
+        else:
+            with torch.cuda.stream(self.stream):
+                kv = torch.empty(shape, dtype=self._dtypes[dtype], device=self.device)
+        k, v = kv.unbind(0)
+        _bs._check(_on_device(self.device, self.stream, self._read, self._ref, _bs.DTYPES[dtype],
+                              slots.data_ptr(), n, k.data_ptr(), v.data_ptr()), "bs_kvq_read")
         return k, v
 
 
@@ -305,17 +323,15 @@ class CacheAttention:
 
     def __init__(self, batch, rows, heads, kv_heads, head_dim, block_size, max_blocks,
                  max_prompt_blocks=0, q_len=1, dtype="bf16", scale=None, stream=None):
-        import torch
+        torch = _t()
         cfg = bs_cache_attn_config(batch, rows, q_len, heads, kv_heads, head_dim, block_size,
                                    max_blocks, max_prompt_blocks, _bs.DTYPES[dtype],
                                    head_dim ** -0.5 if scale is None else scale)
         self.cfg, self._lib = cfg, attn_library()
         self.device = _gpu_device(stream)
         h = ctypes.c_void_p()
-        with _on(self.device):
-            _bs._check(self._lib.bs_cache_attn_create(ctypes.addressof(cfg),
-                                                      _bs._stream(stream), ctypes.addressof(h)),
-                       "bs_cache_attn_create")
+        _bs._check(_on_device(self.device, stream, lambda raw: self._lib.bs_cache_attn_create(
+            ctypes.addressof(cfg), raw, ctypes.addressof(h))), "bs_cache_attn_create")
         self.h = h.value
         self._rows, self._n = batch * rows, batch * rows * q_len
         self.out = torch.empty((self._n, heads, head_dim), dtype=_torch_dtypes()[dtype],
@@ -375,39 +391,49 @@ class CrossAttention:
 
     def __init__(self, batch, max_rows, heads, kv_heads, head_dim, max_keys, dtype="bf16",
                  scale=None, stream=None):
-        import torch
+        torch = _t()
         cfg = bs_cross_attn_config(batch, max_rows, heads, kv_heads, head_dim, max_keys,
                                    _bs.DTYPES[dtype], head_dim ** -0.5 if scale is None else scale)
         self.cfg, self._lib = cfg, attn_library()
         self.device = _gpu_device(stream)
         h = ctypes.c_void_p()
-        with _on(self.device):
-            _bs._check(self._lib.bs_cross_attn_create(ctypes.addressof(cfg),
-                                                      _bs._stream(stream), ctypes.addressof(h)),
-                       "bs_cross_attn_create")
+        _bs._check(_on_device(self.device, stream, lambda raw: self._lib.bs_cross_attn_create(
+            ctypes.addressof(cfg), raw, ctypes.addressof(h))), "bs_cross_attn_create")
         self.h = h.value
         self._buf = torch.empty(batch * max_rows * heads * head_dim, dtype=_torch_dtypes()[dtype],
                                 device=self.device)
         self._i32, self._mask_types = torch.int32, (torch.uint8, torch.bool)
+        self._outs = {}  # the views of _buf by their rows
+        self._kv = bs_cross_kv()
+        self._kv_ref = ctypes.addressof(self._kv)
 
     def __call__(self, q, k, v, lens=None, mask=None, out=None):
         c, dev = self.cfg, self.device
         dt = self._buf.dtype
-        for t, what in ((q, "q"), (k, "k"), (v, "v")):
-            _need(t, what, dev, dt)
+        _need(q, "q", dev, dt)
+        _need(k, "k", dev, dt)
+        _need(v, "v", dev, dt)
         if q.dim() != 4 or not q.shape[1] <= c.max_rows:
             raise ValueError(f"q: shape {list(q.shape)}, at most {c.max_rows} rows")
         rows = q.shape[1]
         stride = _head_rows(q, "q", (c.batch, rows), c.heads, c.head_dim)
         n = k.shape[1] if k.dim() == 4 else -1
-        if tuple(k.shape) != (c.batch, n, c.kv_heads, c.head_dim) or v.shape != k.shape or \
+        if k.shape != (c.batch, n, c.kv_heads, c.head_dim) or v.shape != k.shape or \
                 n > c.max_keys:
             raise ValueError(f"k, v: shapes {list(k.shape)}, {list(v.shape)}, expected two "
                              f"[{c.batch}, at most {c.max_keys}, {c.kv_heads}, {c.head_dim}]")
-        ks, vs = ([s if size > 1 else 0 for s, size in zip(t.stride()[:3], t.shape)] for t in (k, v))
-        if ks != vs or k.stride(3) != 1 or v.stride(3) != 1:
-            raise ValueError("k, v: equal strides and a contiguous last dimension are needed")
-        kv = bs_cross_kv(k.data_ptr() or None, v.data_ptr() or None, *ks)
+        kv = self._kv
+        if k.is_contiguous() and v.is_contiguous():
+            kv.head_stride = c.head_dim
+            kv.pos_stride = c.kv_heads * c.head_dim
+            kv.batch_stride = n * kv.pos_stride
+        else:
+            ks, vs = ([s if size > 1 else 0 for s, size in zip(t.stride()[:3], t.shape)]
+                      for t in (k, v))
+            if ks != vs or k.stride(3) != 1 or v.stride(3) != 1:
+                raise ValueError("k, v: equal strides and a contiguous last dimension are needed")
+            kv.batch_stride, kv.pos_stride, kv.head_stride = ks
+        kv.k, kv.v = k.data_ptr() or None, v.data_ptr() or None
         lp = mp = None
         ms = n
         if lens is not None:
@@ -421,11 +447,14 @@ class CrossAttention:
             ms = mask.stride(0) if c.batch > 1 else n
             mp = mask.data_ptr() or None
         if out is None:
-            out = self._buf[:c.batch * rows * c.heads * c.head_dim].view(q.shape)
+            out = self._outs.get(rows)
+            if out is None:
+                out = self._outs[rows] = \
+                    self._buf[:c.batch * rows * c.heads * c.head_dim].view(q.shape)
         else:
             _need(out, "out", dev, dt, tuple(q.shape))
         _bs._check(self._lib.bs_cross_attn(self.h, q.data_ptr() or None, stride, rows,
-                                           ctypes.addressof(kv), n, lp, mp, ms,
+                                           self._kv_ref, n, lp, mp, ms,
                                            out.data_ptr() or None), "bs_cross_attn")
         return out
 
