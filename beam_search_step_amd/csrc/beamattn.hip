@@ -306,12 +306,16 @@ int bs_map_blocks(void* hip_stream, int32_t n, int32_t block_size, int32_t max_b
   a.cu = cu;
   a.slots = slots;
   a.used = used;
-  a.per = (n + 511) / 512;
+  // four requests or more to a workgroup, one to a wave at a time, of 512 tokens
+  // or more each
+  a.per = (n + 1023) / 1024;
+  a.per = a.per < kAttnWaves ? kAttnWaves : a.per;
   a.chunks = (n + a.per - 1) / a.per;
   const int tails = max_tokens > 0 ? 1 : 0;
-  int parts = (int)((max_tokens / (int64_t)a.chunks + 2047) / 2048);
-  const int most = 1024 / a.chunks > 1 ? 1024 / a.chunks : 1;
-  a.parts = parts < 1 ? 1 : parts > most ? most : parts;
+  a.shift = (block_size & (block_size - 1)) == 0 ? __builtin_ctz(block_size) : -1;
+  const int64_t parts = max_tokens / ((int64_t)n * 512);
+  const int most = 2048 / a.chunks;
+  a.parts = parts < 1 ? 1 : parts > most ? most : (int)parts;
   hipLaunchKernelGGL(m1_map, dim3(a.chunks + tails, a.parts), dim3(kAttnThreads), 0,
                      (hipStream_t)hip_stream, a);
   return launch_status();
