@@ -14,7 +14,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
 constexpr int kAttnThreads = 256;
-constexpr int kAttnWaves = kAttnThreads / 64;
+constexpr int kAttnWaves = kAttnThreads / 64;  // of the kernels that take no NW
 constexpr int kStep = 32;        // keys of one step of a wave
 constexpr int kMaxSplits = 64;   // partial sums joined per query and head
 
@@ -110,10 +110,10 @@ struct Softmax {
 
 // The sums of a workgroup's waves, joined in LDS in wave order, then the
 // result or the workgroup's partial. One barrier: the waves write side by side.
-template <int DP, int NM>
+template <int DP, int NM, int NW>
 struct JoinLds {
-  float acc[kAttnWaves][16 * NM][DP + 4];
-  float m[kAttnWaves][16 * NM], l[kAttnWaves][16 * NM];
+  float acc[NW][16 * NM][DP + 4];
+  float m[NW][16 * NM], l[NW][16 * NM];
 };
 
 template <typename T>
@@ -130,8 +130,8 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* p, f32x4 v) {
 
 // Columns [col0, col0 + 16 NM) of `cols`; column / group is a query row behind
 // row0, the rest a head behind head0. Every thread of the workgroup calls it.
-template <int DP, int NM, typename TO>
-__device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, NM>& lds,
+template <int DP, int NM, int NW, typename TO>
+__device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, NM, NW>& lds,
                                                f32x4 (&acc)[NM][DP / 16], Softmax<NM>& sm,
                                                int col0, int cols, int64_t row0, int head0,
                                                int split) {
@@ -157,17 +157,17 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
             f32x4{acc[i][j][r], acc[i][j + 1][r], acc[i][j + 2][r], acc[i][j + 3][r]};
     }
   __syncthreads();
-  for (int idx = tid; idx < 16 * NM * (DP / 4); idx += kAttnThreads) {
+  for (int idx = tid; idx < 16 * NM * (DP / 4); idx += NW * 64) {
     const int x = idx / (DP / 4), d = (idx - x * (DP / 4)) * 4;
     const int col = col0 + x;
     if (col >= cols || d >= a.D) continue;
     float M = lds.m[0][x];
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) M = fmaxf(M, lds.m[w][x]);
+    for (int w = 1; w < NW; ++w) M = fmaxf(M, lds.m[w][x]);
     float L = 0.0f;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float mw = lds.m[w][x];
       const float f = mw == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mw - M);
       L += f * lds.l[w][x];

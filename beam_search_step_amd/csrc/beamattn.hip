@@ -43,6 +43,7 @@ struct bs_cache_attn_state {
   bs_cache_attn_config cfg;
   hipStream_t stream;
   int device;
+  int nm, nw;          // 16-column tiles of a wave, waves of a workgroup
   int splits[2];       // workgroups along the keys: of a prompt, of a row
   float* block;        // the partial sums
   float* pml;
@@ -129,14 +130,30 @@ KvqPool kvq_pool(const bs_kvq_desc* c) {
 
 // Workgroups along the keys: enough for kWantGroups in the launch, each with
 // kMinKeys at least.
-constexpr int kWantGroups = 1024;
+constexpr int kWantGroups = 768;
 constexpr int kMinKeys = 256;
 int choose_splits(int64_t groups, int64_t keys, int most) {
   int64_t s = (kWantGroups + groups - 1) / groups;
+  // chunks of more than 2048 keys: a third more of them, so that the last
+  // workgroups of ragged lengths are not late (8 prompts of 16,000 to 48,000
+  // tokens: 124 us against 131; 1500-key sources are 22 us with three chunks, 25
+  // with four)
+  if (keys > 2048 * s) s = (kWantGroups + kWantGroups / 3 + groups - 1) / groups;
   const int64_t by_keys = (keys + kMinKeys - 1) / kMinKeys;
   if (s > by_keys) s = by_keys;
   if (s > most) s = most;
   return s < 1 ? 1 : (int)s;
+}
+
+// Waves of a workgroup, for the kernels of one column tile. One where units are
+// short and so many that a wave each fills the device (the wide search's 16 beams
+// of 16 heads over 128 positions: 30 us, with four waves 34). Eight where there are
+// units enough to go without partial sums and the launch that joins them: 64
+// sequences of 8 heads and 500 keys, 15.8 us against 20; 1000-key fp32 sources of
+// 16 by 16 heads, 38 against 40. Four else.
+int choose_waves(int64_t pairs, int64_t keys, bool one_kind) {
+  if (pairs >= 2048 && keys <= 512) return 1;
+  return one_kind && pairs >= 256 && keys > 256 ? 8 : 4;
 }
 
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -204,59 +221,78 @@ int launch_combine(const QueryArgs& q, int64_t units, int dtype, hipStream_t s) 
 }
 
 template <int DP, int NM, int NT>
-void launch_cache_u(const CacheArgs& a, dim3 grid, hipStream_t s) {
-  if (a.bs % 16 == 0)
-    hipLaunchKernelGGL((a1_cache<DP, NM, NT, true>), grid, dim3(kAttnThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((a1_cache<DP, NM, NT, false>), grid, dim3(kAttnThreads), 0, s, a);
+void launch_cache_u(const CacheArgs& a, int nw, dim3 grid, hipStream_t s) {
+  if (a.bs % 16) {
+    hipLaunchKernelGGL((a1_cache<DP, NM, 4, NT, false>), grid, dim3(256), 0, s, a);
+    return;
+  }
+  if constexpr (NM == 1 && DP < 256) {
+    if (nw == 1) {
+      hipLaunchKernelGGL((a1_cache<DP, NM, 1, NT, true>), grid, dim3(64), 0, s, a);
+      return;
+    }
+    if (nw == 8) {
+      hipLaunchKernelGGL((a1_cache<DP, NM, 8, NT, true>), grid, dim3(512), 0, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((a1_cache<DP, NM, 4, NT, true>), grid, dim3(256), 0, s, a);
 }
 template <int DP, int NT>
-void launch_cache_n(const CacheArgs& a, int nm, dim3 grid, hipStream_t s) {
+void launch_cache_n(const CacheArgs& a, int nm, int nw, dim3 grid, hipStream_t s) {
   constexpr int MOST = cache_most<DP, NT>();
   if constexpr (MOST >= 4)
-    if (nm == 4) return launch_cache_u<DP, 4, NT>(a, grid, s);
+    if (nm == 4) return launch_cache_u<DP, 4, NT>(a, nw, grid, s);
   if constexpr (MOST >= 2)
-    if (nm == 2) return launch_cache_u<DP, 2, NT>(a, grid, s);
-  launch_cache_u<DP, 1, NT>(a, grid, s);
+    if (nm == 2) return launch_cache_u<DP, 2, NT>(a, nw, grid, s);
+  launch_cache_u<DP, 1, NT>(a, nw, grid, s);
 }
-void launch_cache(const CacheArgs& a, int dtype, int nm, dim3 grid, hipStream_t s) {
+void launch_cache(const CacheArgs& a, int dtype, int nm, int nw, dim3 grid, hipStream_t s) {
   const int dp = pad_dim(a.q.D);
   if (dtype == BS_BF16) {
-    if (dp == 64) launch_cache_n<64, 1>(a, nm, grid, s);
-    else if (dp == 128) launch_cache_n<128, 1>(a, nm, grid, s);
-    else launch_cache_n<256, 1>(a, nm, grid, s);
+    if (dp == 64) launch_cache_n<64, 1>(a, nm, nw, grid, s);
+    else if (dp == 128) launch_cache_n<128, 1>(a, nm, nw, grid, s);
+    else launch_cache_n<256, 1>(a, nm, nw, grid, s);
   } else {
-    if (dp == 64) launch_cache_n<64, 3>(a, nm, grid, s);
-    else if (dp == 128) launch_cache_n<128, 3>(a, nm, grid, s);
-    else launch_cache_n<256, 3>(a, nm, grid, s);
+    if (dp == 64) launch_cache_n<64, 3>(a, nm, nw, grid, s);
+    else if (dp == 128) launch_cache_n<128, 3>(a, nm, nw, grid, s);
+    else launch_cache_n<256, 3>(a, nm, nw, grid, s);
   }
 }
 
+template <int DP, int NM, typename T>
+void launch_cross_w(const CrossArgs& a, int nw, dim3 grid, hipStream_t s) {
+  if constexpr (NM == 1 && DP < 256) {
+    if (nw == 1) {
+      hipLaunchKernelGGL((a2_cross<DP, NM, 1, T>), grid, dim3(64), 0, s, a);
+      return;
+    }
+    if (nw == 8) {
+      hipLaunchKernelGGL((a2_cross<DP, NM, 8, T>), grid, dim3(512), 0, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((a2_cross<DP, NM, 4, T>), grid, dim3(256), 0, s, a);
+}
 template <int DP, typename T>
-void launch_cross_n(const CrossArgs& a, int nm, dim3 grid, hipStream_t s) {
+void launch_cross_n(const CrossArgs& a, int nm, int nw, dim3 grid, hipStream_t s) {
   constexpr int MOST = cross_most<DP, T>();
   if constexpr (MOST >= 4)
-    if (nm == 4) {
-      hipLaunchKernelGGL((a2_cross<DP, 4, T>), grid, dim3(kAttnThreads), 0, s, a);
-      return;
-    }
+    if (nm == 4) return launch_cross_w<DP, 4, T>(a, nw, grid, s);
   if constexpr (MOST >= 2)
-    if (nm == 2) {
-      hipLaunchKernelGGL((a2_cross<DP, 2, T>), grid, dim3(kAttnThreads), 0, s, a);
-      return;
-    }
-  hipLaunchKernelGGL((a2_cross<DP, 1, T>), grid, dim3(kAttnThreads), 0, s, a);
+    if (nm == 2) return launch_cross_w<DP, 2, T>(a, nw, grid, s);
+  launch_cross_w<DP, 1, T>(a, nw, grid, s);
 }
-void launch_cross(const CrossArgs& a, int dtype, int nm, dim3 grid, hipStream_t s) {
+void launch_cross(const CrossArgs& a, int dtype, int nm, int nw, dim3 grid, hipStream_t s) {
   const int dp = pad_dim(a.q.D);
   if (dtype == BS_BF16) {
-    if (dp == 64) launch_cross_n<64, uint16_t>(a, nm, grid, s);
-    else if (dp == 128) launch_cross_n<128, uint16_t>(a, nm, grid, s);
-    else launch_cross_n<256, uint16_t>(a, nm, grid, s);
+    if (dp == 64) launch_cross_n<64, uint16_t>(a, nm, nw, grid, s);
+    else if (dp == 128) launch_cross_n<128, uint16_t>(a, nm, nw, grid, s);
+    else launch_cross_n<256, uint16_t>(a, nm, nw, grid, s);
   } else {
-    if (dp == 64) launch_cross_n<64, float>(a, nm, grid, s);
-    else if (dp == 128) launch_cross_n<128, float>(a, nm, grid, s);
-    else launch_cross_n<256, float>(a, nm, grid, s);
+    if (dp == 64) launch_cross_n<64, float>(a, nm, nw, grid, s);
+    else if (dp == 128) launch_cross_n<128, float>(a, nm, nw, grid, s);
+    else launch_cross_n<256, float>(a, nm, nw, grid, s);
   }
 }
 
@@ -446,15 +482,19 @@ int bs_cache_attn_create(const bs_cache_attn_config* cfg, void* hip_stream,
   const int64_t rg = ((int64_t)c.q_len * group + 16 * nm - 1) / (16 * nm);
   const int64_t pw = (int64_t)c.batch * c.kv_heads * pg;
   const int64_t rw = (int64_t)c.batch * c.rows * c.kv_heads * rg;
-  const int sp = c.max_prompt_blocks ? choose_splits(pw, (int64_t)c.max_prompt_blocks * c.block_size,
-                                                     kMaxSplits / 2)
-                                     : 0;
-  const int sr = choose_splits(rw, (int64_t)c.max_blocks * c.block_size, kMaxSplits / 2);
+  const int64_t pk = (int64_t)c.max_prompt_blocks * c.block_size;
+  const int64_t rk = (int64_t)c.max_blocks * c.block_size;
+  const bool one_tile = nm == 1 && c.block_size % 16 == 0 && c.head_dim <= 128;
+  const int nw = one_tile ? choose_waves(rw, pk > rk ? pk : rk, !c.max_prompt_blocks) : 4;
+  const int sp = !c.max_prompt_blocks ? 0 : nw == 4 ? choose_splits(pw, pk, kMaxSplits / 2) : 1;
+  const int sr = nw == 4 ? choose_splits(rw, rk, kMaxSplits / 2) : 1;
   if (pw * sp + rw * sr > kMaxGridX) return BS_EINVAL;
   bs_cache_attn_state* h = (bs_cache_attn_state*)calloc(1, sizeof(bs_cache_attn_state));
   if (!h) return BS_ENOMEM;
   h->cfg = c;
   h->stream = (hipStream_t)hip_stream;
+  h->nm = nm;
+  h->nw = nw;
   h->splits[0] = sp;
   h->splits[1] = sr;
   if (hipGetDevice(&h->device) != hipSuccess) {
@@ -488,9 +528,7 @@ int bs_cache_attn(bs_cache_attn_state* h, const bs_kvq_desc* cache, const void* 
   if (!prompt_table != !prompt_lens || (prompt_table && !c.max_prompt_blocks)) return BS_EINVAL;
   OnDevice on(h->device);
   if (!on.ok) return BS_EDEVICE;
-  const int nm = column_tiles((int64_t)(c.max_prompt_blocks ? c.rows : 1) * c.q_len *
-                                  (c.heads / c.kv_heads),
-                              cache_tiles_most(pad_dim(c.head_dim), c.dtype));
+  const int nm = h->nm;
   CacheArgs a;
   a.q = query_args(q, q_stride, c.heads, c.kv_heads, c.head_dim, c.scale, out);
   a.k = (const uint8_t*)cache->k;
@@ -528,7 +566,7 @@ int bs_cache_attn(bs_cache_attn_state* h, const bs_kvq_desc* cache, const void* 
   a.q.ns = sp + sr;
   a.q.pml = h->pml;
   a.q.pacc = h->pacc;
-  launch_cache(a, c.dtype, nm, dim3(p.blocks + r.blocks), h->stream);
+  launch_cache(a, c.dtype, nm, h->nw, dim3(p.blocks + r.blocks), h->stream);
   int rc = launch_status();
   if (rc == BS_OK && a.q.ns > 1)
     rc = launch_combine(a.q, (int64_t)c.batch * c.rows * c.q_len * c.heads, c.dtype, h->stream);
@@ -620,7 +658,8 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   a.groups = (int)((cols + per - 1) / per);
   const int64_t units = (int64_t)c.batch * n_rows * c.heads;
   const int64_t wg = (int64_t)(tile ? (a.pairs + 7) / 8 * 8 : a.pairs) * a.groups;
-  a.splits = choose_splits(wg, n_keys, kMaxSplits);
+  const int nw = nm == 1 && c.head_dim <= 128 && !tile ? choose_waves(wg, n_keys, true) : 4;
+  a.splits = nw == 4 ? choose_splits(wg, n_keys, kMaxSplits) : 1;
   if (a.splits > 1 && units * a.splits > h->units) {
     a.splits = (int)(h->units / units);
     if (a.splits < 1) a.splits = 1;
@@ -633,7 +672,7 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   if (tile)
     launch_tile(a, grid, h->stream);
   else
-    launch_cross(a, c.dtype, nm, grid, h->stream);
+    launch_cross(a, c.dtype, nm, nw, grid, h->stream);
   int rc = launch_status();
   if (rc == BS_OK && a.splits > 1) rc = launch_combine(a.q, units, c.dtype, h->stream);
   return rc;

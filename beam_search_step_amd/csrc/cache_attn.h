@@ -184,11 +184,13 @@ __device__ __forceinline__ void widen_v(const RawKv<DP>& x, bf16x8 (&vf)[DP / 16
   gather_v<VD>(rows, vf);
 }
 
-template <int DP, int NM, int NT, bool UNI>
-__global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
+// One wave a workgroup and 64 values: registers for five waves a SIMD, so that the
+// wide search's 4352 workgroups are all resident (30 us against 32).
+template <int DP, int NM, int NW, int NT, bool UNI>
+__global__ __launch_bounds__(NW * 64, NW == 1 && DP == 64 ? 5 : 1) void a1_cache(CacheArgs a) {
   using TO = typename std::conditional<NT == 1, uint16_t, float>::type;
   constexpr int NP = NT == 1 ? 2 : 3;
-  __shared__ JoinLds<DP, NM> lds;
+  __shared__ JoinLds<DP, NM, NW> lds;
   const int lane = threadIdx.x & 63, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int idx = blockIdx.x;
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
   const int len = min(max(s.lens[unit], 0), s.mb * a.bs);
   // the keys of this split: 128 (a step of each wave) times a whole number
   int per = (len + s.splits - 1) / s.splits;
-  per = (per + kAttnWaves * kStep - 1) / (kAttnWaves * kStep) * (kAttnWaves * kStep);
+  per = (per + NW * kStep - 1) / (NW * kStep) * (NW * kStep);
   const int begin = min((int64_t)sp * per, (int64_t)len), end = min(begin + per, len);
   const int* trow = s.table + (int64_t)unit * s.table_stride;
 
@@ -232,7 +234,7 @@ __global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
     RawKv<DP> cur;
     load_step<DP, UNI>(a, trow, len, n0, h, cur);
     while (true) {
-      const int n1 = n0 + kAttnWaves * kStep;
+      const int n1 = n0 + NW * kStep;
       const bool more = n1 < end;
       if (cur.bm) {
         int lim[NM];
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(kAttnThreads) void a1_cache(CacheArgs a) {
       n0 = n1;
     }
   }
-  join_and_store<DP, NM, TO>(a.q, lds, acc, sm, col0, cols, row0, head0, s.split0 + sp);
+  join_and_store<DP, NM, NW, TO>(a.q, lds, acc, sm, col0, cols, row0, head0, s.split0 + sp);
 }
 
 }  // namespace

@@ -218,10 +218,10 @@ __device__ __forceinline__ void step_f32(const QueryF32<DP, NM>& q, Softmax<NM>&
   }
 }
 
-template <int DP, int NM, typename T>
-__global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
+template <int DP, int NM, int NW, typename T>
+__global__ __launch_bounds__(NW * 64) void a2_cross(CrossArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
-  __shared__ JoinLds<DP, NM> lds;
+  __shared__ JoinLds<DP, NM, NW> lds;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int idx = blockIdx.x;
   const int sp = idx % a.splits;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
   const int head0 = h * a.q.group;
   const int len = a.lens ? min(max(a.lens[b], 0), a.n_keys) : a.n_keys;
   int per = (len + a.splits - 1) / a.splits;
-  per = (per + kAttnWaves * kStep - 1) / (kAttnWaves * kStep) * (kAttnWaves * kStep);
+  per = (per + NW * kStep - 1) / (NW * kStep) * (NW * kStep);
   const int begin = min((int64_t)sp * per, (int64_t)len), end = min(begin + per, len);
   const char* kb = a.k + b * a.batch_stride + h * a.head_stride;
   const char* vb = a.v + b * a.batch_stride + h * a.head_stride;
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
     typename std::conditional<F32, RawF32<DP>, RawBf16<DP>>::type cur;
     load_step<DP>(a, kb, vb, mrow, len, n0, cur);
     while (true) {
-      const int n1 = n0 + kAttnWaves * kStep;
+      const int n1 = n0 + NW * kStep;
       const bool more = n1 < end;
       if (cur.bm) {
         if constexpr (F32) {
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kAttnThreads) void a2_cross(CrossArgs a) {
       n0 = n1;
     }
   }
-  join_and_store<DP, NM, T>(a.q, lds, acc, sm, col0, cols, row0, head0, sp);
+  join_and_store<DP, NM, NW, T>(a.q, lds, acc, sm, col0, cols, row0, head0, sp);
 }
 
 }  // namespace
