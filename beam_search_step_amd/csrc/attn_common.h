@@ -110,6 +110,8 @@ struct Softmax {
 
 // The sums of a workgroup's waves, joined in LDS in wave order, then the
 // result or the workgroup's partial. One barrier: the waves write side by side.
+// Nothing was seen where the sum is zero (a maximum of -inf does not say so: that
+// of scores that are all NaN is -inf too, and their sum NaN).
 template <int DP, int NM, int NW>
 struct JoinLds {
   float acc[NW][16 * NM][DP + 4];
@@ -164,19 +166,19 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
     float M = lds.m[0][x];
 #pragma unroll
     for (int w = 1; w < NW; ++w) M = fmaxf(M, lds.m[w][x]);
+    const float ref = M == -kInf ? 0.0f : M;
     float L = 0.0f;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float mw = lds.m[w][x];
-      const float f = mw == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mw - M);
+      const float f = __builtin_amdgcn_exp2f(lds.m[w][x] - ref);
       L += f * lds.l[w][x];
       v += f * *reinterpret_cast<f32x4*>(&lds.acc[w][x][d]);
     }
     const int qr = fast_div(a.by_group, col);
     const int64_t u = (row0 + qr) * a.heads + head0 + (col - qr * a.group);
     if (a.ns == 1) {
-      const float f = M == -kInf ? 0.0f : __builtin_amdgcn_rcpf(L);
+      const float f = L == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(L);
       store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v * f);
     } else {
       if (d == 0) {
@@ -184,7 +186,7 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
         p[0] = M;
         p[1] = L;
       }
-      if (M != -kInf) store4(a.pacc + (u * a.ns + split) * a.D + d, v);
+      if (L != 0.0f) store4(a.pacc + (u * a.ns + split) * a.D + d, v);
     }
   }
 }
@@ -220,22 +222,22 @@ __global__ __launch_bounds__(kAttnThreads) void a_combine(CombineArgs a) {
     float top = M;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, y[k].x);
-    if (top == -kInf) continue;
-    const float f = M == -kInf ? 0.0f : __builtin_amdgcn_exp2f(M - top);
+    const float ref = top == -kInf ? 0.0f : top;
+    const float f = __builtin_amdgcn_exp2f(M - ref);
     L *= f;
     v *= f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       // a split that saw nothing left its sums unwritten
-      if (s0 + k >= a.ns || y[k].x == -kInf) continue;
-      const float w = __builtin_amdgcn_exp2f(y[k].x - top);
+      if (s0 + k >= a.ns || y[k].y == 0.0f) continue;
+      const float w = __builtin_amdgcn_exp2f(y[k].x - ref);
       L += w * y[k].y;
       v += w * x[k];
     }
     M = top;
   }
-  const float f = M == -kInf ? 0.0f : __builtin_amdgcn_rcpf(L);
-  store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, M == -kInf ? f32x4{0, 0, 0, 0} : v * f);
+  const float f = L == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(L);
+  store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v * f);
 }
 
 // ---------------------------------------------------------------------------

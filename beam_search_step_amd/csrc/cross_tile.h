@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
     l = as_f(sw[0]) + as_f(sw[1]);
   }
   if (col >= cols) return;
-  const bool none = m == -kInf;
+  const bool none = l == 0.0f;  // all-NaN scores leave m at -inf, but not l at zero
   const float f = none ? 0.0f : 1.0f / l;
   if (a.q.ns > 1 && hh == 0) {
     float* p = a.q.pml + (unit * a.q.ns + sp) * 2;

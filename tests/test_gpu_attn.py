@@ -364,6 +364,47 @@ def test_cross_attention_infinite_scores(dev):
         ref.check(out, want, tol, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows, keys", [(1, 1), (3, 40), (3, 3000), (150, 70)])
+def test_cross_attention_nan_is_not_lost(dev, dtype, rows, keys):
+    """A NaN query makes its own row NaN, and a seen NaN key its item's rows, also where
+    every score of a row is NaN."""
+    import beam_search_step_amd as bs
+    g = torch.Generator().manual_seed(rows + keys)
+    q, k, v = [torch.randn(s, generator=g).to(DT[dtype]) for s in ((3, rows, 2, 64), (3, keys, 2, 64), (3, keys, 2, 64))]
+    q[0, rows // 2, 1, 5] = math.nan
+    k[2, keys - 1, 0, 9] = math.nan
+    say("nan", dtype, rows, keys)
+    out = bs.CrossAttention(3, rows, 2, 2, 64, keys, dtype)(q.to(dev), k.to(dev), v.to(dev))
+    want, tol = ref.cross_attention(q.double(), k.double(), v.double(), None, None, 0.125, dtype)
+    assert torch.isnan(want).sum() == 64 * (1 + rows)
+    ref.check(out, want, tol, "NaN")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 5])
+@pytest.mark.parametrize("heads, q_len, prompt, gen", [(2, 1, 0, 1), (4, 1, 30, 9), (2, 1, 40, 700), (2, 3, 0, 20)])
+def test_cache_attention_nan_is_not_lost(dev, dtype, block, heads, q_len, prompt, gen):
+    import beam_search_step_amd as bs
+    mb, pmb = -(-gen // block), -(-prompt // block)
+    cache, vals, _ = make_cache(dev, 2 * mb + pmb, block, 2, 64, 3)
+    table = [list(range(mb)), list(range(mb, 2 * mb))]
+    ptable = [list(range(2 * mb, 2 * mb + pmb))] if prompt else None
+    q = torch.randn((2 * q_len, heads, 64), generator=torch.Generator().manual_seed(4)).to(DT[dtype])
+    q[0, 1, 5] = math.nan
+    at = table[1][0], 0, 1, 9                     # seen by every query of the second row
+    cache.k[at] = 0x7f
+    vals[0][at] = math.nan
+    say("nan", dtype, block, heads, q_len, prompt, gen)
+    att = bs.CacheAttention(1, 2, heads, 2, 64, block, mb, pmb, q_len, dtype)
+    kw = dict(prompt_table=i32(ptable, dev), prompt_lens=i32([prompt], dev)) if prompt else {}
+    out = att(q.to(dev), cache, i32(table, dev), i32([gen, gen], dev), **kw)
+    want, tol = ref.cache_attention(q.double(), *vals, table, [gen, gen], ptable, [prompt] if prompt else None,
+                                    q_len, 2, 0.125, dtype)
+    assert torch.isnan(want).sum() == 64 * (1 + q_len * heads // 2)
+    ref.check(out, want, tol, "NaN")
+
+
 # --- the operators together ---------------------------------------------------
 
 def test_search_with_a_quantised_paged_cache(dev):
