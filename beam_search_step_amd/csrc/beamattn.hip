@@ -297,11 +297,24 @@ void launch_cross(const CrossArgs& a, int dtype, int nm, int nw, dim3 grid, hipS
 }
 
 constexpr int64_t kTileCols = 64;  // more columns than this share keys through LDS
-void launch_tile(const CrossArgs& a, dim3 grid, hipStream_t s) {
+// Waves of 32 columns in its workgroup. Eight, which bring a tile in for twice the
+// columns, where they are a workgroup for every CU at least (the rate at 32 heads of
+// 128 is 320 us against 333); heads of 256 leave registers for four.
+int tile_waves(int64_t pairs, int64_t cols, int dp) {
+  return dp <= 128 && cols > 128 && pairs * ((cols + 255) / 256) >= 256 ? 8 : 4;
+}
+void launch_tile(const CrossArgs& a, int nw, dim3 grid, hipStream_t s) {
   const int dp = pad_dim(a.q.D);
-  if (dp == 64) hipLaunchKernelGGL(a3_tile<64>, grid, dim3(kAttnThreads), 0, s, a);
-  else if (dp == 128) hipLaunchKernelGGL(a3_tile<128>, grid, dim3(kAttnThreads), 0, s, a);
-  else hipLaunchKernelGGL(a3_tile<256>, grid, dim3(kAttnThreads), 0, s, a);
+  const dim3 blk(64 * nw);
+  if (dp == 64) {
+    if (nw == 8) hipLaunchKernelGGL((a3_tile<64, 8>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((a3_tile<64, 4>), grid, blk, 0, s, a);
+  } else if (dp == 128) {
+    if (nw == 8) hipLaunchKernelGGL((a3_tile<128, 8>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((a3_tile<128, 4>), grid, blk, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((a3_tile<256, 4>), grid, blk, 0, s, a);
+  }
 }
 
 // one allocation: the maxima and sums, then the partial sums
@@ -653,8 +666,9 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   const int64_t cols = (int64_t)n_rows * a.q.group;
   const int nm = column_tiles(cols, cross_tiles_most(pad_dim(c.head_dim), c.dtype));
   const bool tile = c.dtype == BS_BF16 && cols > kTileCols;
-  const int per = tile ? 128 : 16 * nm;
   a.pairs = c.batch * c.kv_heads;
+  const int tw = tile_waves(a.pairs, cols, pad_dim(c.head_dim));
+  const int per = tile ? 32 * tw : 16 * nm;
   a.groups = (int)((cols + per - 1) / per);
   const int64_t units = (int64_t)c.batch * n_rows * c.heads;
   const int64_t wg = (int64_t)(tile ? (a.pairs + 7) / 8 * 8 : a.pairs) * a.groups;
@@ -670,7 +684,7 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   a.q.pacc = h->pacc;
   const dim3 grid((unsigned)(wg * a.splits));
   if (tile)
-    launch_tile(a, grid, h->stream);
+    launch_tile(a, tw, grid, h->stream);
   else
     launch_cross(a, c.dtype, nm, nw, grid, h->stream);
   int rc = launch_status();

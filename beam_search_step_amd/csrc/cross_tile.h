@@ -7,97 +7,139 @@ namespace {
 
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
-// 128 columns (a column: one query of one head of the group) over all keys, or a
-// split of them; every wave has 32 columns, and the workgroup's four share tiles
-// of KT keys through LDS. With lane = 32 hh + x:
+// 32 NW columns (a column: one query of one head of the group) over all keys, or
+// a split of them; every wave has 32 columns, and the workgroup's share tiles of KT
+// keys through LDS. With lane = 32 hh + x:
 //   S^T = K Q^T   A: row x is key 32 t + x, values 16 s + 8 hh + e of step s; B:
 //                 column x; the result's register 4 b + r, half hh is key 32 t +
 //                 8 b + 4 hh + r
 //   O^T = V^T P^T 16 keys at a time: index 8 hh + 4 b + r is key 16 kk + 8 b +
 //                 4 hh + r, so that P^T is what the lane holds; A: row x of tile
-//                 j is value VD x + j, the result's register 4 b + r value
-//                 VD (8 b + 4 hh + r) + j
-// K lies in LDS as its operands, the rows of step s and half hh permuted by
-// x ^ (2 s + hh), so that neither the writes (16 chunks of a row at once) nor the
-// reads (32 rows of a chunk) meet in a bank. V lies as its operands too: a thread
-// turns 4 keys by 8 values into 8 values by 4 keys on the way in.
+//                 j is value 32 j + x, read transposed from LDS; the result's
+//                 register 4 b + r is value 32 j + 8 b + 4 hh + r
+// The next tile's loads go straight to LDS while this one is used, so they take no
+// registers, no instructions to turn V, and no writes. 8 items of 1024 rows over
+// 2048 keys, 32 heads of 128: 320 us, 860 TFLOP/s; through registers, V turned on
+// the way, 345. The matrix units are busy 42 % of the time: between two barriers
+// (4200 cycles, 1024 of them a wave's matrix instructions) the waves meet at the
+// loads (32 KB at the 64 bytes a cycle that a CU takes in), the exponentials, and
+// the barrier. Tried and no better: scores of the next tile during this one's
+// exponentials, two tiles between barriers, priorities for the matrix phases.
 template <int DP>
 struct TileLds {
   static constexpr int KT = 8192 / DP;   // keys of a tile: 16 KB of K and of V
   u32x4 k[2][1024];
-  u32x2 v[2][2048];
+  u32x4 v[2][1024];
 };
 
+// Chunk c (eight values) of a key lies at c ^ swizzle of its row, so that the 16
+// rows of one chunk that a read of K takes at once, and the 4 rows by 4 chunks of
+// a read of V, lie in different banks.
 template <int DP>
-struct TileRegs {
-  u32x4 k[4], v[4];
-  uint64_t lo, hi;   // keys of the tile that are seen
+__device__ __forceinline__ int swizzle_k(int key) {
+  return DP == 64 ? (key >> 1) & 7 : key & 15;
+}
+template <int DP>
+__device__ __forceinline__ int swizzle_v(int key) {
+  return DP == 64 ? 4 * ((key >> 1) & 1) : 4 * (key & 3);
+}
+
+struct SeenBits {
+  uint64_t lo, hi;   // keys of a tile that are seen; bits past the tile are set
+  __device__ bool all() const { return lo == ~(uint64_t)0 && hi == ~(uint64_t)0; }
 };
-
-template <int DP>
-__device__ __forceinline__ void tile_load(const CrossArgs& a, const char* kb, const char* vb,
-                                          const uint8_t* mrow, int len, int n0, TileRegs<DP>& x) {
-  constexpr int CH = DP / 8, KT = TileLds<DP>::KT;
-  const int tid = threadIdx.x, lane = tid & 63, D = a.q.D;
-  const char* kp = kb + (int64_t)n0 * a.pos_stride;
-  const char* vp = vb + (int64_t)n0 * a.pos_stride;
-  const int last = len - 1 - n0;  // keys past the length: the last one again
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int idx = i * kAttnThreads + tid, key = idx / CH, d = idx % CH * 8;
-    x.k[i] = *reinterpret_cast<const u32x4*>(kp + (min(key, last) * a.pos_stride + (d < D ? 2 * d : 0)));
-    if (d >= D) x.k[i] = u32x4{0, 0, 0, 0};
+template <int KT>
+__device__ __forceinline__ SeenBits tile_bits(const uint8_t* mrow, int len, int n0) {
+  SeenBits x = {~(uint64_t)0, ~(uint64_t)0};
+  const int left = len - n0, lane = threadIdx.x & 63;
+  if (mrow || left < KT) {
+    bool a = lane < left, b = lane + 64 < left;
+    if (mrow && a && lane < KT) a = mrow[n0 + lane] != 0;
+    if (mrow && b && KT > 64) b = mrow[n0 + lane + 64] != 0;
+    x.lo = __ballot(a || lane >= KT);
+    x.hi = __ballot(b || KT <= 64);
   }
-  const int d = tid % CH * 8, k0 = tid / CH * 4;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    x.v[r] = *reinterpret_cast<const u32x4*>(vp + (min(k0 + r, last) * a.pos_stride + (d < D ? 2 * d : 0)));
-  x.lo = x.hi = ~(uint64_t)0;
-  if (mrow || last < KT - 1) {
-    bool ok = lane <= last, ok2 = lane + 64 <= last;
-    if (mrow && ok) ok = mrow[n0 + lane] != 0;
-    if (mrow && ok2 && KT > 64) ok2 = mrow[n0 + lane + 64] != 0;
-    x.lo = __ballot(ok);
-    x.hi = __ballot(ok2);
-  }
-}
-template <int DP>
-__device__ __forceinline__ bool tile_full(const TileRegs<DP>& x) {
-  constexpr int KT = TileLds<DP>::KT;
-  const uint64_t all = ~(uint64_t)0;
-  return KT == 32 ? (uint32_t)x.lo == ~0u : x.lo == all && (KT == 64 || x.hi == all);
+  return x;
 }
 
-template <int DP>
-__device__ __forceinline__ void tile_store(TileLds<DP>& lds, int buf, TileRegs<DP>& x) {
-  constexpr int CH = DP / 8, VD = DP / 32;
-  const int tid = threadIdx.x;
+// A tile's K or V straight into LDS: a load of a wave fills 64 chunks in a row,
+// 16 bytes a lane, whole keys side by side. `off` is the lane's byte offset in a
+// tile: the swizzles of keys 64 NW / CH apart are alike up to 16 chunks a key, with
+// 32 there are two kinds.
+template <int DP, int NW>
+struct TileOffs {
+  static constexpr int N = DP == 256 ? 2 : 1;
+  int k[N], v[N];
+  __device__ void init(int pos_stride, int D) {
+    constexpr int CH = DP / 8;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int key = wave * (64 / CH) + lane / CH;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int idx = i * kAttnThreads + tid, key = idx / CH, c = idx % CH;
-    lds.k[buf][((key >> 5) * (CH / 2) + (c >> 1)) * 64 + (c & 1) * 32 + ((key & 31) ^ c)] = x.k[i];
+    for (int i = 0; i < N; ++i) {
+      const int ck = (lane % CH) ^ swizzle_k<DP>(key + i * (64 * NW / CH));
+      const int cv = (lane % CH) ^ swizzle_v<DP>(key + i * (64 * NW / CH));
+      k[i] = key * pos_stride + (8 * ck < D ? 16 * ck : 0);
+      v[i] = key * pos_stride + (8 * cv < D ? 16 * cv : 0);
+    }
   }
-  const int c = tid % CH, kg = tid / CH;
-  if (!tile_full(x)) {  // the values of a key that is not seen are zero
-    const uint64_t bits = kg < 16 ? x.lo >> (4 * kg) : x.hi >> (4 * (kg - 16));
+};
+// the tile of keys n0 .., K at kp and V at vp; past the length: the last key again
+template <int DP, int NW>
+__device__ __forceinline__ void tile_load(const TileOffs<DP, NW>& off, const char* kp, const char* vp,
+                                          int pos_stride, int len, int n0, u32x4* k, u32x4* v) {
+  constexpr int CH = DP / 8, KT = TileLds<DP>::KT, N = TileOffs<DP, NW>::N, M = 16 / NW;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int last = len - 1 - n0;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (!((bits >> r) & 1)) x.v[r] = u32x4{0, 0, 0, 0};
+  for (int i = 0; i < 2 * M; ++i) {
+    const int ii = i % M, add = ii * (64 * NW / CH);
+    const char* p = (i < M ? kp : vp) + (int64_t)add * pos_stride;
+    int o = i < M ? off.k[ii % N] : off.v[ii % N];
+    if (last < KT - 1) {
+      const int key = wave * (64 / CH) + lane / CH;
+      o += (min(key + add, last) - (key + add)) * pos_stride;
+    }
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(p + o),
+                                     (__attribute__((address_space(3))) void*)((i < M ? k : v) + (ii * NW + wave) * 64),
+                                     16, 0, 0);
   }
-  const int kk = kg >> 2, b = (kg >> 1) & 1, hh = kg & 1;
+}
+// Waits for this wave's loads, and clears what a product must not meet: K past the
+// head's values, the values of keys that are not seen.
+template <int DP, int NW>
+__device__ __forceinline__ void tile_ready(int D, SeenBits seen, u32x4* k, u32x4* v) {
+  constexpr int CH = DP / 8;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if (D < DP) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-    const u32x2 w = {__builtin_amdgcn_perm(x.v[1][j / 2], x.v[0][j / 2], sel),
-                     __builtin_amdgcn_perm(x.v[3][j / 2], x.v[2][j / 2], sel)};
-    const int d = 8 * c + j;
-    lds.v[buf][((kk * VD + d % VD) * 64 + hh * 32 + d / VD) * 2 + b] = w;
+    for (int i = 0; i < 16 / NW; ++i) {
+      const int key = (i * NW + wave) * (64 / CH) + lane / CH;
+      if (8 * ((lane % CH) ^ swizzle_k<DP>(key)) >= D)
+        k[(i * NW + wave) * 64 + lane] = u32x4{0, 0, 0, 0};
+    }
+  }
+  if (!seen.all()) {
+#pragma unroll
+    for (int i = 0; i < 16 / NW; ++i) {
+      const int key = (i * NW + wave) * (64 / CH) + lane / CH;
+      if (!(((key < 64 ? seen.lo : seen.hi) >> (key & 63)) & 1))
+        v[(i * NW + wave) * 64 + lane] = u32x4{0, 0, 0, 0};
+    }
   }
 }
 
-template <int DP>
-__global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(CrossArgs a) {
-  constexpr int KT = TileLds<DP>::KT, NT = KT / 32, VD = DP / 32, NS = DP / 16;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+// 4 keys by 16 values, the lanes of a group of 16 holding 4 values each, four lanes
+// to a key: lane i gets value i of the four keys.
+__device__ __forceinline__ s16x4 read_transposed(const char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+}
+
+template <int DP, int NW>
+__global__ __launch_bounds__(NW * 64, DP == 256 ? 1 : 2) void a3_tile(CrossArgs a) {
+  constexpr int KT = TileLds<DP>::KT, NT = KT / 32, VD = DP / 32, NS = DP / 16, CH = DP / 8;
   __shared__ TileLds<DP> lds;
   const int tid = threadIdx.x, lane = tid & 63, hh = lane >> 5, x = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -121,7 +163,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
   const char* vb = a.v + b * a.batch_stride + h * a.head_stride;
   const uint8_t* mrow = a.mask ? a.mask + b * a.mask_stride : nullptr;
 
-  const int col = grp * 128 + wave * 32 + x, qc = min(col, cols - 1);
+  const int col = (grp * NW + wave) * 32 + x, qc = min(col, cols - 1);
   const int qr = fast_div(a.q.by_group, qc);
   const int64_t unit = (row0 + qr) * a.q.heads + head0 + (qc - qr * a.q.group);
   bf16x8 q[NS];
@@ -146,18 +188,33 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
   bf16x2 ones;
   ones.x = ones.y = (__bf16)1.0f;
 
-  TileRegs<DP> in;
+  // this lane's places in a tile: K's row x, chunk 2 s + hh; V's row 4 hh + y / 4 of
+  // 16 kk + 8 b .., values 32 j + 16 (x / 16) + 4 (y % 4) .., y the lane in its 16
+  const int y = lane & 15, vrow = 4 * hh + (y >> 2);
+  const int vlane = vrow * DP * 2 + ((2 * (x >> 4) + ((y & 3) >> 1)) * 16 + (y & 1) * 8);
+  const int ksw = swizzle_k<DP>(x), vsw = swizzle_v<DP>(vrow);
+
+  TileOffs<DP, NW> off;
+  off.init(a.pos_stride, a.q.D);
+  kb += (int64_t)begin * a.pos_stride;
+  vb += (int64_t)begin * a.pos_stride;
+  SeenBits seen = {0, 0};
   if (begin < end) {
-    tile_load<DP>(a, kb, vb, mrow, len, begin, in);
-    tile_store<DP>(lds, 0, in);
+    seen = tile_bits<KT>(mrow, len, begin);
+    tile_load<DP, NW>(off, kb, vb, a.pos_stride, len, begin, lds.k[0], lds.v[0]);
+    tile_ready<DP, NW>(a.q.D, seen, lds.k[0], lds.v[0]);
   }
   __syncthreads();
   int buf = 0;
   for (int n0 = begin; n0 < end; n0 += KT, buf ^= 1) {
-    const bool full = tile_full(in);
-    const uint64_t lo = in.lo, hi = in.hi;
+    const SeenBits now = seen;
     const bool more = n0 + KT < end;
-    if (more) tile_load<DP>(a, kb, vb, mrow, len, n0 + KT, in);
+    if (more) {
+      seen = tile_bits<KT>(mrow, len, n0 + KT);
+      kb += (int64_t)KT * a.pos_stride;
+      vb += (int64_t)KT * a.pos_stride;
+      tile_load<DP, NW>(off, kb, vb, a.pos_stride, len, n0 + KT, lds.k[buf ^ 1], lds.v[buf ^ 1]);
+    }
     f32x16 st[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -165,14 +222,14 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
       for (int r = 0; r < 16; ++r) st[t][r] = 0.0f;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const u32x4 w = lds.k[buf][(t * NS + s) * 64 + hh * 32 + (x ^ (2 * s + hh))];
+        const u32x4 w = lds.k[buf][(32 * t + x) * CH + ((2 * s + hh) ^ ksw)];
         st[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), q[s], st[t], 0, 0, 0);
       }
     }
-    if (!full) {
+    if (!now.all()) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint32_t bits = (uint32_t)((t < 2 ? lo : hi) >> (32 * (t & 1))) >> (4 * hh);
+        const uint32_t bits = (uint32_t)((t < 2 ? now.lo : now.hi) >> (32 * (t & 1))) >> (4 * hh);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (!((bits >> (8 * (r >> 2) + (r & 3))) & 1)) st[t][r] = -kInf;
@@ -187,17 +244,20 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
       auto sw = __builtin_amdgcn_permlane32_swap(as_u(top), as_u(top), false, false);
       top = fmaxf(as_f(sw[0]), as_f(sw[1])) * c;
     }
-    const float mn = fmaxf(m, top);
-    const float ref = mn == -kInf ? 0.0f : mn;
-    if (__ballot(mn != m)) {
-      const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    // the point that scores are taken from follows the maximum only when it is
+    // 2^8 behind: probabilities keep their relative rounding, and far from the
+    // 2^127 that sums hold
+    if (__ballot(top > m + 8.0f)) {
+      const float mn = fmaxf(m, top);
+      const float alpha = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
       l *= alpha;
 #pragma unroll
       for (int j = 0; j < VD; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[j][r] *= alpha;
+      m = mn;
     }
-    m = mn;
+    const float ref = m == -kInf ? 0.0f : m;
     // the sum is of the rounded probabilities, those that the product uses
     bf16x8 pf[2 * NT];
 #pragma unroll
@@ -221,11 +281,14 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
     for (int kk = 0; kk < 2 * NT; ++kk)
 #pragma unroll
       for (int j = 0; j < VD; ++j) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(
-            &lds.v[buf][((kk * VD + j) * 64 + hh * 32 + x) * 2]);
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), pf[kk], acc[j], 0, 0, 0);
+        const char* p = reinterpret_cast<const char*>(lds.v[buf]) + vlane + ((4 * j) ^ vsw) * 16 +
+                        16 * kk * DP * 2;
+        const s16x4 lo = read_transposed(p), hi = read_transposed(p + 8 * DP * 2);
+        const bf16x8 w = __builtin_bit_cast(
+            bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, pf[kk], acc[j], 0, 0, 0);
       }
-    if (more) tile_store<DP>(lds, buf ^ 1, in);
+    if (more) tile_ready<DP, NW>(a.q.D, seen, lds.k[buf ^ 1], lds.v[buf ^ 1]);
     __syncthreads();
   }
 
@@ -244,12 +307,12 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : 2) void a3_tile(Cross
 #pragma unroll
   for (int bb = 0; bb < 4; ++bb)
 #pragma unroll
-    for (int i = 0; i < VD; ++i) {  // four values each: VD (8 bb + 4 hh) + 4 i ..
-      const int d = VD * (8 * bb + 4 * hh) + 4 * i;
+    for (int j = 0; j < VD; ++j) {
+      const int d = 32 * j + 8 * bb + 4 * hh;
       if (d >= a.q.D) continue;
       f32x4 v;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = acc[(4 * i + k) % VD][4 * bb + (4 * i + k) / VD];
+      for (int k = 0; k < 4; ++k) v[k] = acc[j][4 * bb + k];
       if (a.q.ns > 1) {
         if (!none) store4(a.q.pacc + (unit * a.q.ns + sp) * a.q.D + d, v);
       } else {

@@ -257,6 +257,17 @@ def test_cache_attention(dev, case, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [
+    (2, 3, 1, 2, 2, 128, 16, 90, 200), (1, 1, 1, 1, 1, 96, 32, 0, 1300), (2, 1, 1, 3, 3, 48, 16, 30, 65),
+    (1, 1, 1, 2, 2, 128, 16, 33, 600), (4, 64, 1, 8, 8, 64, 16, 40, 20), (4, 64, 1, 16, 8, 64, 16, 17, 70),
+    (2, 128, 2, 8, 8, 128, 16, 0, 35), (2, 128, 1, 8, 8, 112, 16, 33, 40), (32, 1, 1, 8, 8, 64, 16, 0, 300),
+    (32, 1, 1, 16, 8, 128, 16, 0, 270), (32, 1, 1, 8, 8, 128, 32, 0, 333), (32, 1, 3, 8, 8, 80, 16, 0, 290),
+])
+def test_cache_attention_of_one_column_and_of_many_units(dev, case, dtype):
+    cache_case(dev, *case, dtype, seed=sum(case))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("block", [16, 5])
 def test_cache_attention_skips_bad_entries_and_what_lies_behind(dev, dtype, block):
     cache_case(dev, 2, 2, 1, 4, 2, 64, block, 90, 50, dtype, 77, holes=True, nan_behind=True)
@@ -337,6 +348,30 @@ def cross_case(dev, batch, rows, heads, kv_heads, dim, keys, dtype, seed, lens="
 ])
 def test_cross_attention(dev, case, dtype):
     cross_case(dev, *case, dtype, seed=sum(case))
+
+
+@pytest.mark.parametrize("case", [(32, 130, 8, 8, 64, 270), (16, 300, 8, 8, 128, 131), (32, 70, 16, 8, 80, 33)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_cross_attention_of_many_rows_and_items(dev, case, mask):
+    cross_case(dev, *case, "bf16", seed=sum(case), mask=mask)
+
+
+@pytest.mark.parametrize("rows", [70, 600])
+def test_cross_attention_rising_scores(dev, rows):
+    """Scores that rise and fall by hundreds along the keys: the point that they are
+    taken from has to follow."""
+    import beam_search_step_amd as bs
+    g = torch.Generator().manual_seed(rows)
+    q, k, v = [torch.randn(s, generator=g) for s in ((1, rows, 2, 64), (1, 700, 2, 64), (1, 700, 2, 64))]
+    k[0, :, :, 0] = torch.linspace(-40, 40, 700)[:, None] * torch.tensor([1.0, -1.0])
+    k[0, 300:340, :, 0] = 60.0
+    q[..., 0] = 40.0
+    q[:, ::3, :, 0] = 0.0
+    q, k, v = [x.to(torch.bfloat16) for x in (q, k, v)]
+    say("rising", rows)
+    out = bs.CrossAttention(1, rows, 2, 2, 64, 700, "bf16")(q.to(dev), k.to(dev), v.to(dev))
+    want, tol = ref.cross_attention(q.double(), k.double(), v.double(), None, None, 0.125, "bf16")
+    ref.check(out, want, tol, "rising scores")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
