@@ -43,7 +43,7 @@ struct bs_cache_attn_state {
   bs_cache_attn_config cfg;
   hipStream_t stream;
   int device;
-  int nm, nw;          // 16-column tiles of a wave, waves of a workgroup
+  int nw;              // waves of a workgroup
   int splits[2];       // workgroups along the keys: of a prompt, of a row
   float* block;        // the partial sums
   float* pml;
@@ -158,26 +158,19 @@ int choose_waves(int64_t pairs, int64_t keys, bool one_kind) {
 
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-// 16-column tiles of a wave: as many as the queries fill, and at most as many
-// as its registers hold without spilling (checked in the compiler's report)
-int column_tiles(int64_t cols, int most) {
-  if (cols <= 16 || most == 1) return 1;
-  return cols <= 32 || most == 2 ? 2 : 4;
-}
-template <int DP, int NT>
-constexpr int cache_most() { return NT == 1 ? (DP == 64 ? 4 : DP == 128 ? 2 : 1) : (DP == 64 ? 2 : 1); }
+// 16-column tiles of a wave of a2_cross. Two where keys are worth reading once for
+// both and registers hold them without spilling: 32 columns of 14 items, 8 kv heads
+// of 64 and 1403 bf16 keys are 19 us, one tile at a time 23; 4096 columns of 512 fp32
+// keys 388 us against 575 and with four tiles 461.
 template <int DP, typename T>
-constexpr int cross_most() { return DP == 64 ? 4 : DP == 128 ? 2 : 1; }
-int cache_tiles_most(int dp, int dtype) {
-  if (dtype == BS_BF16)
-    return dp == 64 ? cache_most<64, 1>() : dp == 128 ? cache_most<128, 1>() : cache_most<256, 1>();
-  return dp == 64 ? cache_most<64, 3>() : dp == 128 ? cache_most<128, 3>() : cache_most<256, 3>();
+constexpr int cross_most() {
+  return sizeof(T) == 2 ? (DP == 64 ? 2 : 1) : DP <= 128 ? 2 : 1;
 }
-int cross_tiles_most(int dp, int dtype) {
-  if (dtype == BS_BF16)
-    return dp == 64 ? cross_most<64, uint16_t>()
-                    : dp == 128 ? cross_most<128, uint16_t>() : cross_most<256, uint16_t>();
-  return dp == 64 ? cross_most<64, float>() : dp == 128 ? cross_most<128, float>() : cross_most<256, float>();
+// fp32 heads of 128: 56 columns of 1403 keys are 110 us one tile at a time and 116
+// two, 4096 columns of 512 keys 1170 and 1006
+int cross_tiles(int64_t cols, int dp, int dtype) {
+  if (cols <= 16 || dp == 256) return 1;
+  return dp == 64 || (dtype == BS_F32 && cols > 64) ? 2 : 1;
 }
 
 QueryArgs query_args(const void* q, int64_t q_stride, int heads, int kv_heads, int D, double scale,
@@ -220,43 +213,34 @@ int launch_combine(const QueryArgs& q, int64_t units, int dtype, hipStream_t s) 
   return launch_status();
 }
 
-template <int DP, int NM, int NT>
+template <int DP, int NT>
 void launch_cache_u(const CacheArgs& a, int nw, dim3 grid, hipStream_t s) {
   if (a.bs % 16) {
-    hipLaunchKernelGGL((a1_cache<DP, NM, 4, NT, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((a1_cache<DP, 4, NT, false>), grid, dim3(256), 0, s, a);
     return;
   }
-  if constexpr (NM == 1 && DP < 256) {
+  if constexpr (DP < 256) {
     if (nw == 1) {
-      hipLaunchKernelGGL((a1_cache<DP, NM, 1, NT, true>), grid, dim3(64), 0, s, a);
+      hipLaunchKernelGGL((a1_cache<DP, 1, NT, true>), grid, dim3(64), 0, s, a);
       return;
     }
     if (nw == 8) {
-      hipLaunchKernelGGL((a1_cache<DP, NM, 8, NT, true>), grid, dim3(512), 0, s, a);
+      hipLaunchKernelGGL((a1_cache<DP, 8, NT, true>), grid, dim3(512), 0, s, a);
       return;
     }
   }
-  hipLaunchKernelGGL((a1_cache<DP, NM, 4, NT, true>), grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL((a1_cache<DP, 4, NT, true>), grid, dim3(256), 0, s, a);
 }
-template <int DP, int NT>
-void launch_cache_n(const CacheArgs& a, int nm, int nw, dim3 grid, hipStream_t s) {
-  constexpr int MOST = cache_most<DP, NT>();
-  if constexpr (MOST >= 4)
-    if (nm == 4) return launch_cache_u<DP, 4, NT>(a, nw, grid, s);
-  if constexpr (MOST >= 2)
-    if (nm == 2) return launch_cache_u<DP, 2, NT>(a, nw, grid, s);
-  launch_cache_u<DP, 1, NT>(a, nw, grid, s);
-}
-void launch_cache(const CacheArgs& a, int dtype, int nm, int nw, dim3 grid, hipStream_t s) {
+void launch_cache(const CacheArgs& a, int dtype, int nw, dim3 grid, hipStream_t s) {
   const int dp = pad_dim(a.q.D);
   if (dtype == BS_BF16) {
-    if (dp == 64) launch_cache_n<64, 1>(a, nm, nw, grid, s);
-    else if (dp == 128) launch_cache_n<128, 1>(a, nm, nw, grid, s);
-    else launch_cache_n<256, 1>(a, nm, nw, grid, s);
+    if (dp == 64) launch_cache_u<64, 1>(a, nw, grid, s);
+    else if (dp == 128) launch_cache_u<128, 1>(a, nw, grid, s);
+    else launch_cache_u<256, 1>(a, nw, grid, s);
   } else {
-    if (dp == 64) launch_cache_n<64, 3>(a, nm, nw, grid, s);
-    else if (dp == 128) launch_cache_n<128, 3>(a, nm, nw, grid, s);
-    else launch_cache_n<256, 3>(a, nm, nw, grid, s);
+    if (dp == 64) launch_cache_u<64, 3>(a, nw, grid, s);
+    else if (dp == 128) launch_cache_u<128, 3>(a, nw, grid, s);
+    else launch_cache_u<256, 3>(a, nw, grid, s);
   }
 }
 
@@ -277,8 +261,6 @@ void launch_cross_w(const CrossArgs& a, int nw, dim3 grid, hipStream_t s) {
 template <int DP, typename T>
 void launch_cross_n(const CrossArgs& a, int nm, int nw, dim3 grid, hipStream_t s) {
   constexpr int MOST = cross_most<DP, T>();
-  if constexpr (MOST >= 4)
-    if (nm == 4) return launch_cross_w<DP, 4, T>(a, nw, grid, s);
   if constexpr (MOST >= 2)
     if (nm == 2) return launch_cross_w<DP, 2, T>(a, nw, grid, s);
   launch_cross_w<DP, 1, T>(a, nw, grid, s);
@@ -296,7 +278,11 @@ void launch_cross(const CrossArgs& a, int dtype, int nm, int nw, dim3 grid, hipS
   }
 }
 
-constexpr int64_t kTileCols = 64;  // more columns than this share keys through LDS
+// bf16: more columns than this share keys through LDS, of 14 items of 8 kv heads and
+// 1403 keys: 56 columns of 64 values 26 us against 40, 32 columns 25 against 20; 56
+// of 128 values 35 against 61, 32 columns of 96 29 against 37; 56 of 256 values 88
+// against 118, 24 columns 80 against 78.
+int tile_cols(int dp) { return dp == 128 ? 16 : 32; }
 // Waves of 32 columns in its workgroup. Eight, which bring a tile in for twice the
 // columns, where they are a workgroup for every CU at least (the rate at 32 heads of
 // 128 is 320 us against 333); heads of 256 leave registers for four.
@@ -489,16 +475,14 @@ int bs_cache_attn_create(const bs_cache_attn_config* cfg, void* hip_stream,
       (int64_t)c.block_size * c.max_prompt_blocks >= ((int64_t)1 << 31))
     return BS_EINVAL;
   const int group = c.heads / c.kv_heads;
-  const int nm = column_tiles((int64_t)(c.max_prompt_blocks ? c.rows : 1) * c.q_len * group,
-                              cache_tiles_most(pad_dim(c.head_dim), c.dtype));
-  const int64_t pg = ((int64_t)c.rows * c.q_len * group + 16 * nm - 1) / (16 * nm);
-  const int64_t rg = ((int64_t)c.q_len * group + 16 * nm - 1) / (16 * nm);
+  const int64_t pg = ((int64_t)c.rows * c.q_len * group + 15) / 16;
+  const int64_t rg = ((int64_t)c.q_len * group + 15) / 16;
   const int64_t pw = (int64_t)c.batch * c.kv_heads * pg;
   const int64_t rw = (int64_t)c.batch * c.rows * c.kv_heads * rg;
   const int64_t pk = (int64_t)c.max_prompt_blocks * c.block_size;
   const int64_t rk = (int64_t)c.max_blocks * c.block_size;
-  const bool one_tile = nm == 1 && c.block_size % 16 == 0 && c.head_dim <= 128;
-  const int nw = one_tile ? choose_waves(rw, pk > rk ? pk : rk, !c.max_prompt_blocks) : 4;
+  const bool uniform = c.block_size % 16 == 0 && c.head_dim <= 128;
+  const int nw = uniform ? choose_waves(rw, pk > rk ? pk : rk, !c.max_prompt_blocks) : 4;
   const int sp = !c.max_prompt_blocks ? 0 : nw == 4 ? choose_splits(pw, pk, kMaxSplits / 2) : 1;
   const int sr = nw == 4 ? choose_splits(rw, rk, kMaxSplits / 2) : 1;
   if (pw * sp + rw * sr > kMaxGridX) return BS_EINVAL;
@@ -506,7 +490,6 @@ int bs_cache_attn_create(const bs_cache_attn_config* cfg, void* hip_stream,
   if (!h) return BS_ENOMEM;
   h->cfg = c;
   h->stream = (hipStream_t)hip_stream;
-  h->nm = nm;
   h->nw = nw;
   h->splits[0] = sp;
   h->splits[1] = sr;
@@ -541,7 +524,6 @@ int bs_cache_attn(bs_cache_attn_state* h, const bs_kvq_desc* cache, const void* 
   if (!prompt_table != !prompt_lens || (prompt_table && !c.max_prompt_blocks)) return BS_EINVAL;
   OnDevice on(h->device);
   if (!on.ok) return BS_EDEVICE;
-  const int nm = h->nm;
   CacheArgs a;
   a.q = query_args(q, q_stride, c.heads, c.kv_heads, c.head_dim, c.scale, out);
   a.k = (const uint8_t*)cache->k;
@@ -563,7 +545,7 @@ int bs_cache_attn(bs_cache_attn_state* h, const bs_kvq_desc* cache, const void* 
   p.back = 0;
   p.splits = sp;
   p.split0 = 0;
-  p.groups = (int)(((int64_t)p.qrows * a.q.group + 16 * nm - 1) / (16 * nm));
+  p.groups = (int)(((int64_t)p.qrows * a.q.group + 15) / 16);
   p.blocks = c.batch * c.kv_heads * p.groups * sp;
   PagedSeg& r = a.seg[1];
   r.table = table;
@@ -574,12 +556,12 @@ int bs_cache_attn(bs_cache_attn_state* h, const bs_kvq_desc* cache, const void* 
   r.back = c.q_len - 1;
   r.splits = sr;
   r.split0 = sp;
-  r.groups = (c.q_len * a.q.group + 16 * nm - 1) / (16 * nm);
+  r.groups = (c.q_len * a.q.group + 15) / 16;
   r.blocks = c.batch * c.rows * c.kv_heads * r.groups * sr;
   a.q.ns = sp + sr;
   a.q.pml = h->pml;
   a.q.pacc = h->pacc;
-  launch_cache(a, c.dtype, nm, h->nw, dim3(p.blocks + r.blocks), h->stream);
+  launch_cache(a, c.dtype, h->nw, dim3(p.blocks + r.blocks), h->stream);
   int rc = launch_status();
   if (rc == BS_OK && a.q.ns > 1)
     rc = launch_combine(a.q, (int64_t)c.batch * c.rows * c.q_len * c.heads, c.dtype, h->stream);
@@ -664,8 +646,8 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   a.mask = mask;
   a.mask_stride = mask_stride;
   const int64_t cols = (int64_t)n_rows * a.q.group;
-  const int nm = column_tiles(cols, cross_tiles_most(pad_dim(c.head_dim), c.dtype));
-  const bool tile = c.dtype == BS_BF16 && cols > kTileCols;
+  const int nm = cross_tiles(cols, pad_dim(c.head_dim), c.dtype);
+  const bool tile = c.dtype == BS_BF16 && cols > tile_cols(pad_dim(c.head_dim));
   a.pairs = c.batch * c.kv_heads;
   const int tw = tile_waves(a.pairs, cols, pad_dim(c.head_dim));
   const int per = tile ? 32 * tw : 16 * nm;

@@ -15,7 +15,7 @@ struct PagedSeg {
   int qrows;              // query rows of a unit
   int back;               // query i sees lens - back + i positions
   int splits, split0;     // workgroups along the keys, and their first partial
-  int groups;             // groups of 16 NM columns
+  int groups;             // groups of 16 columns
   int blocks;             // workgroups
 };
 
@@ -184,12 +184,24 @@ __device__ __forceinline__ void widen_v(const RawKv<DP>& x, bf16x8 (&vf)[DP / 16
   gather_v<VD>(rows, vf);
 }
 
-// One wave a workgroup and 64 values: registers for five waves a SIMD, so that the
-// wide search's 4352 workgroups are all resident (30 us against 32).
-template <int DP, int NM, int NW, int NT, bool UNI>
-__global__ __launch_bounds__(NW * 64, NW == 1 && DP == 64 ? 5 : 1) void a1_cache(CacheArgs a) {
+// 16 columns a wave: two or four tiles of them read a key once for all, but leave no
+// registers for a second wave (16 items, 16 beams of 4 heads a kv head, prompts of
+// 1000 tokens: 27 us at 64 values a head, with two tiles 38, with four 75; 45 at 128,
+// with two 85).
+// Waves a SIMD that the registers have to leave, as many as go without spilling:
+// left to itself the compiler keeps sums in a second register file and one wave
+// fewer (16 beams of 4 heads a kv head over prompts of 1000 tokens, 256 values a
+// head: two waves 72 us, one 118; 128 fp32 values: three 51, two 67; the wide
+// search's 4352 one-wave workgroups: five, all resident, 30, four 32).
+template <int DP, int NW, int NT, bool UNI>
+constexpr int cache_waves() {
+  return DP == 64 ? (NT == 1 || NW == 1 ? 5 : 4)
+                  : DP == 128 ? (NT == 1 || UNI ? 3 : 2) : NT == 1 ? 2 : 1;
+}
+template <int DP, int NW, int NT, bool UNI>
+__global__ __launch_bounds__(NW * 64, (cache_waves<DP, NW, NT, UNI>())) void a1_cache(CacheArgs a) {
   using TO = typename std::conditional<NT == 1, uint16_t, float>::type;
-  constexpr int NP = NT == 1 ? 2 : 3;
+  constexpr int NM = 1, NP = NT == 1 ? 2 : 3;
   __shared__ JoinLds<DP, NM, NW> lds;
   const int lane = threadIdx.x & 63, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -218,8 +218,15 @@ __device__ __forceinline__ void step_f32(const QueryF32<DP, NM>& q, Softmax<NM>&
   }
 }
 
+// Waves a SIMD that the registers have to leave (fp32 heads of 128, 48 items of 2
+// heads and 4829 keys: two 122 us, one 145).
+template <int DP, int NM, typename T>
+constexpr int cross_waves() {
+  return sizeof(T) == 4 ? (NM == 1 && DP == 128 ? 2 : 1)
+                        : DP == 64 ? (NM == 1 ? 5 : 4) : DP == 128 ? 3 : 1;
+}
 template <int DP, int NM, int NW, typename T>
-__global__ __launch_bounds__(NW * 64) void a2_cross(CrossArgs a) {
+__global__ __launch_bounds__(NW * 64, (cross_waves<DP, NM, T>())) void a2_cross(CrossArgs a) {
   constexpr bool F32 = sizeof(T) == 4;
   __shared__ JoinLds<DP, NM, NW> lds;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

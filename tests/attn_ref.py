@@ -162,7 +162,8 @@ def cache_attention(q, kv, vv, table, lens, ptable, plens, q_len, rows, scale, d
 
 
 def cross_attention(q, k, v, lens, mask, scale, dtype):
-    # bf16 calls of more than 64 columns (rows * grouped heads) round probabilities to bf16
+    # bf16 calls of more than 32 columns (rows * grouped heads; 16 for head sizes from 80
+    # to 128) round probabilities to bf16
     """(values, tolerance) for q [B, R, Hq, D], k, v [B, S, Hkv, D] in float64."""
     b, rows, hq, d = q.shape
     hk = k.shape[2]
@@ -179,7 +180,7 @@ def cross_attention(q, k, v, lens, mask, scale, dtype):
             x = q[i, :, sl].reshape(-1, d)
             seen = torch.ones(x.shape[0], at.numel(), dtype=torch.bool)
             y, t = attend(x, k[i, at, h], v[i, at, h], seen, scale, dtype, 1,
-                          dtype == "bf16" and rows * grp > 64)
+                          dtype == "bf16" and rows * grp > (16 if 64 < d <= 128 else 32))
             o[i, :, sl], tol[i, :, sl] = y.view(rows, grp, d), t.view(rows, grp, d)
     return o, tol
 
