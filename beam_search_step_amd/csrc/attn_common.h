@@ -193,7 +193,8 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
 
 // Joins the partials of one query and head: out = sum_s 2^(m_s - M) acc_s /
 // sum_s 2^(m_s - M) l_s, over those that saw something. LPU lanes take one query
-// and head, four values each, eight partials in flight.
+// and head, four values each, eight partials in flight. A launch's latency bounds it:
+// 32 rows of 32 heads of 128 and 7 partials are 3.9 us.
 struct CombineArgs {
   const float* pacc;
   const float* pml;

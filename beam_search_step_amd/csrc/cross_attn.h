@@ -218,6 +218,8 @@ __device__ __forceinline__ void step_f32(const QueryF32<DP, NM>& q, Softmax<NM>&
   }
 }
 
+// Bound by bandwidth where keys are many and columns few: 16 items of 16 heads of 64,
+// 1500 bf16 keys, 26.7 us, 3.7 TB/s; 1000 fp32 keys 38.7, 3.4 TB/s.
 // Waves a SIMD that the registers have to leave (fp32 heads of 128, 48 items of 2
 // heads and 4829 keys: two 122 us, one 145).
 template <int DP, int NM, typename T>
