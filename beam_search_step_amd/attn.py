@@ -180,7 +180,8 @@ class BlockMap:
         torch = _t()
         self.n, self.block_size, self.max_blocks, self.max_tokens = n, block_size, max_blocks, max_tokens
         if not (1 <= n <= 65535 and block_size >= 1 and max_blocks >= 1 and max_tokens >= 0
-                and block_size * max_blocks < 2 ** 31 and max_tokens < 2 ** 31):
+                and block_size * max_blocks <= 2 ** 31 - 2 ** 21
+                and max_tokens <= 2 ** 31 - 2 ** 21):
             raise ValueError(f"BlockMap({n}, {block_size}, {max_blocks}, {max_tokens})")
         self._fn = attn_library().bs_map_blocks
         self.device = _gpu_device(stream)
@@ -318,7 +319,8 @@ class CacheAttention:
     ``att(q, cache, table, lens, prompt_table=None, prompt_lens=None)`` with q
     [batch * rows * q_len, heads, head_dim] returns the output, of q's shape and
     type: the handle's own tensor, written again by the next call, or ``out``.
-    ``table`` is a tensor [batch * rows, max_blocks] or a PagedKV.
+    ``table`` is a tensor [batch * rows, max_blocks] or a PagedKV. Every call runs
+    on the stream given here, or the one that was current when this was made.
     """
 
     def __init__(self, batch, rows, heads, kv_heads, head_dim, block_size, max_blocks,
@@ -386,7 +388,8 @@ class CrossAttention:
     head_dim] (keys up to max_keys, any strides that keep head_dim contiguous),
     lens int32 [batch], mask uint8 or bool [batch, keys] (nonzero: seen) returns
     the output, of q's shape and type, contiguous: the handle's own memory,
-    written again by the next call, or ``out``.
+    written again by the next call, or ``out``. Every call runs on the stream given
+    here, or the one that was current when this was made.
     """
 
     def __init__(self, batch, max_rows, heads, kv_heads, head_dim, max_keys, dtype="bf16",

@@ -97,8 +97,11 @@ int elem_size(int t) { return t == BS_F32 ? 4 : 2; }
 bool head_dim_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
 bool scale_ok(double s) { return s > 0 && s < 1e30; }
 
-constexpr int64_t kMaxPosStride = (int64_t)1 << 26;  // lane offsets of a step stay below 2^31
+constexpr int64_t kMaxPosStride = (int64_t)1 << 26;   // lane offsets of a step stay below 2^31
+constexpr int64_t kTilePosStride = (int64_t)1 << 24;  // and those of a3_tile's 128 keys
+constexpr int64_t kMaxTokens = 0x7fe00000;  // counters run up to 2^20 past the last token
 constexpr int64_t kMaxGridX = 0xFFFFFFFFll / kAttnThreads;
+bool grid_ok(int64_t groups, int threads) { return groups * threads <= 0xFFFFFFFFll; }
 
 bool kvq_ok(const bs_kvq_desc* c) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return false;
@@ -325,7 +328,7 @@ int bs_map_blocks(void* hip_stream, int32_t n, int32_t block_size, int32_t max_b
                   int32_t max_tokens, int32_t* used) {
   if (n < 1 || n > 65535 || block_size < 1 || max_blocks < 1 || n_free < 0 || max_tokens < 0)
     return BS_EINVAL;
-  if ((int64_t)block_size * max_blocks >= ((int64_t)1 << 31)) return BS_EINVAL;
+  if ((int64_t)block_size * max_blocks > kMaxTokens || max_tokens > kMaxTokens) return BS_EINVAL;
   if (!lens || !table || !cu || !used || (max_tokens > 0 && !slots)) return BS_EINVAL;
   if (n_free > 0 && !free_blocks) return BS_EINVAL;
   MapArgs a;
@@ -358,7 +361,8 @@ int bs_map_blocks(void* hip_stream, int32_t n, int32_t block_size, int32_t max_b
 
 int bs_kvq_write(void* hip_stream, const bs_kvq_desc* cache, int32_t dtype, const void* k,
                  const void* v, int64_t row_stride, const int32_t* slots, int32_t n_tokens) {
-  if (!kvq_ok(cache) || !dtype_ok(dtype) || n_tokens < 0) return BS_EINVAL;
+  if (!kvq_ok(cache) || !dtype_ok(dtype) || n_tokens < 0 || n_tokens > kMaxTokens)
+    return BS_EINVAL;
   if (n_tokens == 0) return BS_OK;
   if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16)) return BS_EINVAL;
   if (row_stride < (int64_t)cache->kv_heads * cache->head_dim ||
@@ -471,8 +475,8 @@ int bs_cache_attn_create(const bs_cache_attn_config* cfg, void* hip_stream,
   if (c.kv_heads < 1 || c.heads < 1 || c.heads > 65535 || c.heads % c.kv_heads) return BS_EINVAL;
   if (!head_dim_ok(c.head_dim) || !dtype_ok(c.dtype) || !scale_ok(c.scale)) return BS_EINVAL;
   if (c.block_size < 1 || c.max_blocks < 1 || c.max_prompt_blocks < 0 ||
-      (int64_t)c.block_size * c.max_blocks >= ((int64_t)1 << 31) ||
-      (int64_t)c.block_size * c.max_prompt_blocks >= ((int64_t)1 << 31))
+      (int64_t)c.block_size * c.max_blocks >= ((int64_t)1 << 30) ||
+      (int64_t)c.block_size * c.max_prompt_blocks >= ((int64_t)1 << 30))
     return BS_EINVAL;
   const int group = c.heads / c.kv_heads;
   const int64_t pg = ((int64_t)c.rows * c.q_len * group + 15) / 16;
@@ -485,7 +489,8 @@ int bs_cache_attn_create(const bs_cache_attn_config* cfg, void* hip_stream,
   const int nw = uniform ? choose_waves(rw, pk > rk ? pk : rk, !c.max_prompt_blocks) : 4;
   const int sp = !c.max_prompt_blocks ? 0 : nw == 4 ? choose_splits(pw, pk, kMaxSplits / 2) : 1;
   const int sr = nw == 4 ? choose_splits(rw, rk, kMaxSplits / 2) : 1;
-  if (pw * sp + rw * sr > kMaxGridX) return BS_EINVAL;
+  const int64_t units = (int64_t)c.batch * c.rows * c.q_len * c.heads;
+  if (!grid_ok(pw * sp + rw * sr, 64 * nw) || units > kMaxGridX * 4) return BS_EINVAL;
   bs_cache_attn_state* h = (bs_cache_attn_state*)calloc(1, sizeof(bs_cache_attn_state));
   if (!h) return BS_ENOMEM;
   h->cfg = c;
@@ -498,8 +503,7 @@ int bs_cache_attn_create(const bs_cache_attn_config* cfg, void* hip_stream,
     return BS_EDEVICE;
   }
   if (sp + sr > 1) {
-    const int64_t units = (int64_t)c.batch * c.rows * c.q_len * c.heads * (sp + sr);
-    const int rc = alloc_partials(units, c.head_dim, &h->block, &h->pml, &h->pacc);
+    const int rc = alloc_partials(units * (sp + sr), c.head_dim, &h->block, &h->pml, &h->pacc);
     if (rc != BS_OK) {
       free(h);
       return rc;
@@ -647,7 +651,8 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
   a.mask_stride = mask_stride;
   const int64_t cols = (int64_t)n_rows * a.q.group;
   const int nm = cross_tiles(cols, pad_dim(c.head_dim), c.dtype);
-  const bool tile = c.dtype == BS_BF16 && cols > tile_cols(pad_dim(c.head_dim));
+  const bool tile = c.dtype == BS_BF16 && cols > tile_cols(pad_dim(c.head_dim)) &&
+                    a.pos_stride < kTilePosStride;
   a.pairs = c.batch * c.kv_heads;
   const int tw = tile_waves(a.pairs, cols, pad_dim(c.head_dim));
   const int per = tile ? 32 * tw : 16 * nm;
@@ -660,7 +665,7 @@ int bs_cross_attn(bs_cross_attn_state* h, const void* q, int64_t q_stride, int32
     a.splits = (int)(h->units / units);
     if (a.splits < 1) a.splits = 1;
   }
-  if (wg * a.splits > kMaxGridX) return BS_EINVAL;
+  if (!grid_ok(wg * a.splits, tile ? 64 * tw : 64 * nw)) return BS_EINVAL;
   a.q.ns = a.splits;
   a.q.pml = h->pml;
   a.q.pacc = h->pacc;

@@ -59,9 +59,9 @@ extern "C" {
  *   used         device int32 [1], written: the blocks asked for, the sum of
  *                want - have (more than n_free: the list ran out); 0 when
  *                free_blocks is NULL
- * Limits: n 1..65535, block_size and max_blocks >= 1 with their product below
- * 2^31; the sums of the lengths and start + len of each request stay below
- * 2^31.
+ * Limits: n 1..65535, block_size and max_blocks >= 1, their product and
+ * max_tokens at most 2^31 - 2^21; the sums of the lengths and start + len of
+ * each request stay below 2^31.
  * Errors: BS_EINVAL; BS_EDEVICE. */
 int bs_map_blocks(void *hip_stream, int32_t n, int32_t block_size, int32_t max_blocks,
                   const int32_t *starts, const int32_t *lens, const int32_t *free_blocks,
@@ -102,7 +102,7 @@ typedef struct {
  *   k, v        device, dtype, rows of kv_heads * head_dim contiguous values
  *   row_stride  elements between tokens (>= kv_heads * head_dim); rows and
  *               row_stride are 16-byte aligned
- *   slots       device int32 [n_tokens]
+ *   slots       device int32 [n_tokens], n_tokens up to 2^31 - 2^21
  * Errors: BS_EINVAL; BS_EDEVICE. */
 int bs_kvq_write(void *hip_stream, const bs_kvq_desc *cache, int32_t dtype, const void *k,
                  const void *v, int64_t row_stride, const int32_t *slots, int32_t n_tokens);
@@ -139,14 +139,15 @@ int bs_kvq_reorder(bs_kv_paged *p, const bs_kvq_desc *layers, int32_t n_layers, 
 typedef struct {
     int32_t batch;             /* B >= 1                                        */
     int32_t rows;              /* rows of an item (beams), >= 1;
-                                  batch * rows * q_len <= 65535                 */
+                                  batch * rows * q_len <= 65535, and times heads
+                                  at most 2^26 - 4                              */
     int32_t q_len;             /* 1..64                                         */
     int32_t heads;             /* a multiple of kv_heads, up to 65535           */
     int32_t kv_heads;          /* >= 1                                          */
     int32_t head_dim;          /* a multiple of 16 up to 256                    */
     int32_t block_size;        /* >= 1                                          */
     int32_t max_blocks;        /* entries of a row's table, >= 1; with the block
-                                  size below 2^31                               */
+                                  size below 2^30                               */
     int32_t max_prompt_blocks; /* entries of an item's prompt table; 0: none    */
     int32_t dtype;             /* of queries and outputs                        */
     double scale;              /* > 0, finite                                   */

@@ -171,3 +171,16 @@ def test_row_layouts_are_checked():
             rows(x, "x", (6,), 2, 64)
     with pytest.raises(ValueError):  # the rows of two items unevenly spaced
         rows(torch.zeros(3, 3, 2, 64)[:, :2], "x", (3, 2), 2, 64)
+
+
+def test_sizes_whose_counters_would_pass_31_bits_are_refused():
+    L, h, d = bs.attn_library(), ctypes.c_void_p(1), _desc()
+    most = (1 << 31) - (1 << 21)
+    assert _map(block_size=1, max_blocks=most + 1) == bs.BS_EINVAL
+    assert _map(max_tokens=most + 1) == bs.BS_EINVAL
+    assert L.bs_kvq_write(None, ctypes.addressof(d), 0, P, P, 128, P, most + 1) == bs.BS_EINVAL
+    for kw in (dict(block_size=1 << 20, max_blocks=1 << 10), dict(block_size=1 << 20, max_prompt_blocks=1 << 10),
+               dict(batch=1, rows=65535, heads=65535, kv_heads=1), dict(batch=1, rows=1025, heads=65532, kv_heads=2)):
+        cfg = _cache_cfg(**kw)
+        assert L.bs_cache_attn_create(ctypes.addressof(cfg), None, ctypes.addressof(h)) == bs.BS_EINVAL, kw
+        assert h.value is None

@@ -704,3 +704,23 @@ def test_offsets_beyond_32_bits(dev):
     out = att(q.to(dev), cache, i32([ids], dev), i32([250], dev))
     want, tol = ref.cache_attention(q.double(), *vals, [[0, 1, 2, 3]], [250], None, None, 1, 1, d ** -0.5, "bf16")
     ref.check(out, want, tol, "far blocks")
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+@pytest.mark.parametrize("shift", [22, 24])
+def test_cross_attention_of_keys_far_apart(dev, rows, shift):
+    """Keys 2^shift elements apart (a batch-inner cache of many items): a key's offset
+    passes 2^31 bytes."""
+    import beam_search_step_amd as bs
+    keys, d = 129, 64
+    g = torch.Generator().manual_seed(shift + rows)
+    q, k, v = [torch.randn(s, generator=g).bfloat16() for s in ((1, rows, 1, d), (1, keys, 1, d), (1, keys, 1, d))]
+    step = 1 << shift
+    pool = torch.empty((keys - 1) * step + 2 * d, dtype=torch.bfloat16, device=dev)
+    kd, vd = [pool[o:].as_strided((1, keys, 1, d), (step, step, d, 1)) for o in (0, d)]
+    kd.copy_(k.to(dev))
+    vd.copy_(v.to(dev))
+    say("far keys", rows, shift)
+    out = bs.CrossAttention(1, rows, 1, 1, d, keys)(q.to(dev), kd, vd)
+    want, tol = ref.cross_attention(q.double(), k.double(), v.double(), None, None, 0.125, "bf16")
+    ref.check(out, want, tol, "far keys")
