@@ -1,6 +1,7 @@
 """The attention-side operators on an MI355X against plain 64-bit references
 (tests/attn_ref.py, where the tolerances are derived)."""
 import math
+import os
 import random
 
 import pytest
@@ -19,7 +20,12 @@ def dev():
     if not torch.cuda.is_available():
         pytest.fail("GPU tests need a GPU")
     torch.cuda.set_device(0)
-    return torch.device("cuda", 0)
+    # an earlier test's CPU timing leaves the process on one core, where a pool of
+    # threads for the references would only wait for itself
+    threads = torch.get_num_threads()
+    torch.set_num_threads(min(threads, len(os.sched_getaffinity(0))))
+    yield torch.device("cuda", 0)
+    torch.set_num_threads(threads)
 
 
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
