@@ -169,8 +169,8 @@ template <int DP, typename T>
 constexpr int cross_most() {
   return sizeof(T) == 2 ? (DP == 64 ? 2 : 1) : DP <= 128 ? 2 : 1;
 }
-// fp32 heads of 128: 56 columns of 1403 keys are 110 us one tile at a time and 116
-// two, 4096 columns of 512 keys 1170 and 1006
+// fp32 heads of 128: 56 columns of 1403 keys are 93 us one tile at a time (two: 116
+// where groups were dealt over the XCDs, one 110), 4096 columns of 512 keys 1170 and 1006
 int cross_tiles(int64_t cols, int dp, int dtype) {
   if (cols <= 16 || dp == 256) return 1;
   return dp == 64 || (dtype == BS_F32 && cols > 64) ? 2 : 1;
