@@ -110,8 +110,10 @@ struct Softmax {
 
 // The sums of a workgroup's waves, joined in LDS in wave order, then the
 // result or the workgroup's partial. One barrier: the waves write side by side.
-// Nothing was seen where the sum is zero (a maximum of -inf does not say so: that
-// of scores that are all NaN is -inf too, and their sum NaN).
+// Nothing was seen, or only scores of -inf, where the sum is zero (a maximum of
+// -inf does not say so: that of scores that are all NaN is -inf too, and their sum
+// NaN). The result is zero then, whatever the values hold; a NaN that a key of no
+// weight brought in is kept until it is known that others have some.
 template <int DP, int NM, int NW>
 struct JoinLds {
   float acc[NW][16 * NM][DP + 4];
@@ -178,21 +180,21 @@ __device__ __forceinline__ void join_and_store(const QueryArgs& a, JoinLds<DP, N
     const int qr = fast_div(a.by_group, col);
     const int64_t u = (row0 + qr) * a.heads + head0 + (col - qr * a.group);
     if (a.ns == 1) {
-      const float f = L == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(L);
-      store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v * f);
+      const float f = __builtin_amdgcn_rcpf(L);
+      store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, L == 0.0f ? f32x4{0, 0, 0, 0} : v * f);
     } else {
       if (d == 0) {
         float* p = a.pml + (u * a.ns + split) * 2;
         p[0] = M;
         p[1] = L;
       }
-      if (L != 0.0f) store4(a.pacc + (u * a.ns + split) * a.D + d, v);
+      store4(a.pacc + (u * a.ns + split) * a.D + d, v);
     }
   }
 }
 
 // Joins the partials of one query and head: out = sum_s 2^(m_s - M) acc_s /
-// sum_s 2^(m_s - M) l_s, over those that saw something. LPU lanes take one query
+// sum_s 2^(m_s - M) l_s, and zero where that is. LPU lanes take one query
 // and head, four values each, eight partials in flight. A launch's latency bounds it:
 // 32 rows of 32 heads of 128 and 7 partials are 3.9 us.
 struct CombineArgs {
@@ -229,16 +231,15 @@ __global__ __launch_bounds__(kAttnThreads) void a_combine(CombineArgs a) {
     v *= f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      // a split that saw nothing left its sums unwritten
-      if (s0 + k >= a.ns || y[k].y == 0.0f) continue;
+      if (s0 + k >= a.ns) continue;
       const float w = __builtin_amdgcn_exp2f(y[k].x - ref);
       L += w * y[k].y;
       v += w * x[k];
     }
     M = top;
   }
-  const float f = L == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(L);
-  store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, v * f);
+  const float f = __builtin_amdgcn_rcpf(L);
+  store4(reinterpret_cast<TO*>(a.out) + u * a.D + d, L == 0.0f ? f32x4{0, 0, 0, 0} : v * f);
 }
 
 // ---------------------------------------------------------------------------

@@ -314,7 +314,7 @@ __global__ __launch_bounds__(NW * 64, DP == 256 ? 1 : 2) void a3_tile(CrossArgs 
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = acc[j][4 * bb + k];
       if (a.q.ns > 1) {
-        if (!none) store4(a.q.pacc + (unit * a.q.ns + sp) * a.q.D + d, v);
+        store4(a.q.pacc + (unit * a.q.ns + sp) * a.q.D + d, v);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = none ? 0.0f : v[k] * f;

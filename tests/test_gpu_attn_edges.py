@@ -1,0 +1,104 @@
+"""Edges of the attention-side operators on an MI355X: infinite scores and values,
+head sizes above 128, scales of blocks that nobody reads, and calls across streams.
+References and tolerances are those of tests/attn_ref.py; cross attention is held to
+the bound of two-term probabilities at every number of columns."""
+import math
+import os
+
+import pytest
+
+import attn_ref as ref
+from test_gpu_attn import i32, make_cache, say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import beam_search_step_amd as bs
+    bs.attn_library()
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    torch.cuda.set_device(0)
+    threads = torch.get_num_threads()
+    torch.set_num_threads(min(threads, len(os.sched_getaffinity(0))))
+    yield torch.device("cuda", 0)
+    torch.set_num_threads(threads)
+
+
+# --- infinite scores and values -----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows, keys", [(1, 40), (1, 3000), (70, 40), (70, 3000), (300, 700)])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_one_key_of_a_score_of_minus_infinity(dev, dtype, rows, keys, dim):
+    """It has no weight: the mean of the others. Scores of the others are 0, so
+    probabilities are exactly equal; n terms in two parts, their sum and the output."""
+    import beam_search_step_amd as bs
+    k = torch.zeros(1, keys, 1, dim)
+    k[0, keys // 2, 0, 5] = -math.inf
+    v = torch.randn(1, keys, 1, dim, generator=torch.Generator().manual_seed(1)).to(DT[dtype])
+    q = torch.ones(1, rows, 1, dim, dtype=DT[dtype], device=dev)
+    say("-inf key", dtype, rows, keys, dim)
+    out = bs.CrossAttention(1, rows, 1, 1, dim, keys, dtype)(q, k.to(DT[dtype]).to(dev), v.to(dev))
+    others = torch.cat([v[0, :keys // 2, 0], v[0, keys // 2 + 1:, 0]]).double()
+    want = others.mean(0)
+    half, extra = (2.0 ** -8, 2.0 ** -15) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -23)
+    tol = half * want.abs() + (extra + (keys + 64) * ref.U) * others.abs().mean(0) * (1 + half)
+    ref.check(out[0, :, 0], want.expand(rows, -1), tol.expand(rows, -1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows, keys", [(1, 1), (1, 40), (1, 3000), (70, 40), (70, 3000)])
+def test_every_score_minus_infinity_gives_zeros(dev, dtype, rows, keys):
+    """Whatever the values hold."""
+    import beam_search_step_amd as bs
+    k = torch.zeros(1, keys, 1, 64)
+    k[..., 5] = -math.inf
+    v = torch.ones(1, keys, 1, 64)
+    v[0, :, 0, 7], v[0, keys // 2, 0, 8], v[0, 0, 0, 9] = math.nan, math.inf, -math.inf
+    q = torch.ones(1, rows, 1, 64)
+    say("all -inf", dtype, rows, keys)
+    out = bs.CrossAttention(1, rows, 1, 1, 64, keys, dtype)(*[x.to(DT[dtype]).to(dev) for x in (q, k, v)])
+    assert torch.equal(out, torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block, prompt, gen", [(16, 0, 5), (16, 40, 9), (5, 30, 700), (16, 0, 1500)])
+def test_every_score_minus_infinity_over_the_cache_gives_zeros(dev, dtype, block, prompt, gen):
+    """Finite queries and keys whose products pass the range of fp32."""
+    import beam_search_step_amd as bs
+    mb, pmb = -(-gen // block), -(-prompt // block)
+    cache, _, _ = make_cache(dev, mb + pmb, block, 1, 64, 2)
+    cache.k.zero_()
+    cache.k[..., 3] = 0x7e                          # 448
+    cache.k_scale.fill_(2.0 ** 20)
+    cache.v[..., 7] = 0x7f                          # NaN
+    q = torch.zeros(1, 2, 64, dtype=DT[dtype], device=dev)
+    q[..., 3] = -3e38
+    att = bs.CacheAttention(1, 1, 2, 1, 64, block, mb, pmb, dtype=dtype)
+    kw = dict(prompt_table=i32([list(range(mb, mb + pmb))], dev), prompt_lens=i32([prompt], dev)) if prompt else {}
+    say("all -inf", dtype, block, prompt, gen)
+    out = att(q, cache, i32([list(range(mb))], dev), i32([gen], dev), **kw)
+    assert torch.equal(out, torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("keys, dead", [(40, 20), (3000, 1536), (3000, 2900)])
+def test_a_nan_value_of_no_weight_is_nan_however_keys_are_split(dev, dtype, rows, keys, dead):
+    """0 * NaN: the first `dead` keys have a score of -inf and a NaN value."""
+    import beam_search_step_amd as bs
+    k = torch.zeros(1, keys, 1, 64)
+    k[0, :dead, 0, 5] = -math.inf
+    v = torch.ones(1, keys, 1, 64)
+    v[0, :dead, 0, 7] = math.nan
+    q = torch.ones(1, rows, 1, 64)
+    say("NaN of no weight", dtype, rows, keys, dead)
+    out = bs.CrossAttention(1, rows, 1, 1, 64, keys, dtype)(*[x.to(DT[dtype]).to(dev) for x in (q, k, v)]).cpu()
+    assert bool(torch.isnan(out[..., 7]).all())
+    rest = torch.cat([out[..., :7], out[..., 8:]], -1).double()
+    assert bool(((rest - 1).abs() <= 2.0 ** -8 + 2.0 ** -15).all())
