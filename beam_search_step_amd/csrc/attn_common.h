@@ -294,8 +294,12 @@ struct QueryBf16 {
   }
 };
 
-// P^T's operand from a lane's eight probabilities, in NP terms.
-template <int NP>
+// P^T's operand from a lane's eight probabilities, in NP terms. Where values can be
+// infinite (INF, two terms), no term of a probability above zero may be zero, since
+// zero times infinity is NaN: the rest of one that the first term holds exactly is
+// 2^-20 of it, a 32nd of what cutting the second term may lose.
+constexpr float kRestUp = 1.0f + 0x1p-20f;
+template <int NP, bool INF>
 __device__ __forceinline__ void split_p(const float (&p)[8], bf16x8 (&f)[NP]) {
   float x[8];
 #pragma unroll
@@ -309,7 +313,8 @@ __device__ __forceinline__ void split_p(const float (&p)[8], bf16x8 (&f)[NP]) {
     f[t] = as_bf16x8(w);
     if (t + 1 < NP) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] -= trunc_bf16(x[e]);
+      for (int e = 0; e < 8; ++e)
+        x[e] = INF ? fmaf(x[e], kRestUp, -trunc_bf16(x[e])) : x[e] - trunc_bf16(x[e]);
     }
   }
 }
@@ -317,8 +322,9 @@ __device__ __forceinline__ void split_p(const float (&p)[8], bf16x8 (&f)[NP]) {
 // One step: load_k and load_v give the two key tiles and the value tiles, the
 // second after the first is used up (registers); bm the step's 32 key bits (a
 // zero bit: the key is not seen, its values are zero). With `causal`, lim[i] is
-// the first key that column i does not see, less the step's first.
-template <int DP, int NM, int NT, int NP, typename LoadK, typename LoadV>
+// the first key that column i does not see, less the step's first. INF: values may
+// be infinite.
+template <int DP, int NM, int NT, int NP, bool INF, typename LoadK, typename LoadV>
 __device__ __forceinline__ void step_bf16(const QueryBf16<DP, NM, NT>& q, Softmax<NM>& sm,
                                           f32x4 (&acc)[NM][DP / 16], LoadK load_k, LoadV load_v,
                                           float c, uint32_t bm, bool causal,
@@ -408,7 +414,7 @@ __device__ __forceinline__ void step_bf16(const QueryBf16<DP, NM, NT>& q, Softma
 #pragma unroll
   for (int i = 0; i < NM; ++i) {
     bf16x8 pf[NP];
-    split_p<NP>(p[i], pf);
+    split_p<NP, INF>(p[i], pf);
 #pragma unroll
     for (int j = 0; j < DP / 16; ++j)
 #pragma unroll

@@ -256,7 +256,7 @@ __global__ __launch_bounds__(NW * 64, (cache_waves<DP, NW, NT, UNI>())) void a1_
         int lim[NM];
 #pragma unroll
         for (int i = 0; i < NM; ++i) lim[i] = first_unseen[i] - n0;
-        step_bf16<DP, NM, NT, NP>(
+        step_bf16<DP, NM, NT, NP, false>(
             q, sm, acc, [&](bf16x8(&kf)[2][DP / 32]) { widen_k<DP>(cur, a.q.D, kf); },
             [&](bf16x8(&vf)[DP / 16]) { widen_v<DP>(cur, vf); }, a.q.c, cur.bm,
             s.back && n0 + kStep > open, lim);

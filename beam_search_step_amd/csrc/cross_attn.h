@@ -294,7 +294,7 @@ __global__ __launch_bounds__(NW * 64, (cross_waves<DP, NM, T>())) void a2_cross(
           step_f32<DP, NM>(q, sm, acc, cur, a.q.c, a.q.D);
         } else {
           const int lim[NM] = {};
-          step_bf16<DP, NM, 1, 2>(
+          step_bf16<DP, NM, 1, 2, true>(
               q, sm, acc, [&](bf16x8(&kf)[2][DP / 32]) { widen_k<DP>(cur, a.q.D, kf); },
               [&](bf16x8(&vf)[DP / 16]) { widen_v<DP>(cur, vf); }, a.q.c, cur.bm, false, lim);
         }

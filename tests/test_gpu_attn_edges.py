@@ -102,3 +102,21 @@ def test_a_nan_value_of_no_weight_is_nan_however_keys_are_split(dev, dtype, rows
     assert bool(torch.isnan(out[..., 7]).all())
     rest = torch.cat([out[..., :7], out[..., 8:]], -1).double()
     assert bool(((rest - 1).abs() <= 2.0 ** -8 + 2.0 ** -15).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 20, 70])
+@pytest.mark.parametrize("keys", [1, 4, 7, 3000])
+def test_infinite_values(dev, dtype, rows, keys):
+    """A seen value of +-inf with some weight is the output, and NaN where both meet."""
+    import beam_search_step_amd as bs
+    v = torch.ones(1, keys, 1, 64)
+    v[0, keys // 2, 0, 7], v[0, 0, 0, 9] = math.inf, -math.inf
+    v[0, 0, 0, 11], v[0, keys - 1, 0, 11] = math.inf, -math.inf
+    q, k = torch.ones(1, rows, 1, 64), torch.zeros(1, keys, 1, 64)
+    say("inf values", dtype, rows, keys)
+    out = bs.CrossAttention(1, rows, 1, 1, 64, keys, dtype)(*[x.to(DT[dtype]).to(dev) for x in (q, k, v)]).cpu()[0, :, 0]
+    assert bool((out[:, 7] == math.inf).all()) and bool((out[:, 9] == -math.inf).all())
+    assert bool((out[:, 11] == -math.inf).all() if keys == 1 else torch.isnan(out[:, 11]).all())
+    rest = torch.cat([out[:, :7], out[:, 12:]], -1).double()
+    assert bool(((rest - 1).abs() <= 2.0 ** -8 + 2.0 ** -15).all())
