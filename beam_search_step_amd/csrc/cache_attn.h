@@ -99,7 +99,8 @@ __device__ __forceinline__ void load_step(const CacheArgs& a, const int* trow, i
         load_words(vp + (min(4 * g + r, last) * a.pos_stride + vd), x.v[4 * t + r]);
       const int64_t si = (int64_t)bid * a.q.kv_heads + h;
       x.ks[t] = a.ks[si];
-      const float vs = a.vs[si];
+      // without a block the scale is another's, perhaps NaN, which a zero would keep
+      const float vs = ok ? a.vs[si] : 1.0f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) x.vs[4 * t + r] = vs;
     }
@@ -114,7 +115,7 @@ __device__ __forceinline__ void load_step(const CacheArgs& a, const int* trow, i
     const int bid = ok ? id : 0;
     const int64_t off = bid * a.block_stride + (int64_t)(ok ? n - kb * a.bs : 0) * a.pos_stride + hd;
     const int64_t si = (int64_t)bid * a.q.kv_heads + h;
-    const float ks = a.ks[si], vs = a.vs[si];
+    const float ks = a.ks[si], vs = ok ? a.vs[si] : 1.0f;  // as above
     x.bm = (uint32_t)__ballot(ok);
     const int lo = (int)(uint32_t)off, hi = (int)(off >> 32);
 #pragma unroll

@@ -120,3 +120,24 @@ def test_infinite_values(dev, dtype, rows, keys):
     assert bool((out[:, 11] == -math.inf).all() if keys == 1 else torch.isnan(out[:, 11]).all())
     rest = torch.cat([out[:, :7], out[:, 12:]], -1).double()
     assert bool(((rest - 1).abs() <= 2.0 ** -8 + 2.0 ** -15).all())
+
+
+# --- scales of blocks that are not read -----------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 5])
+@pytest.mark.parametrize("scale", [math.nan, math.inf, 2.0 ** 127])
+def test_scales_of_blocks_that_no_table_names(dev, dtype, block, scale):
+    """Block 0 was never written; tables have holes and lengths end inside a tile."""
+    import beam_search_step_amd as bs
+    gen, dim, n = 40, 64, 12
+    cache, vals, _ = make_cache(dev, n, block, 2, dim, 6)
+    cache.k_scale[0], cache.v_scale[0] = scale, scale
+    mb = -(-gen // block)
+    table = [list(range(1, 1 + mb)), [-1] + list(range(2, 1 + mb)), list(range(1, mb)) + [n + 7]]
+    lens = [gen, gen, 1]
+    q = torch.randn(3, 4, dim, generator=torch.Generator().manual_seed(8)).to(DT[dtype])
+    say("scales", dtype, block, scale)
+    out = bs.CacheAttention(3, 1, 4, 2, dim, block, mb, dtype=dtype)(q.to(dev), cache, i32(table, dev), i32(lens, dev))
+    want, tol = ref.cache_attention(q.double(), *vals, table, lens, None, None, 1, 1, dim ** -0.5, dtype)
+    ref.check(out, want, tol, "scales")
