@@ -279,6 +279,9 @@ struct QueryBf16 {
           const f32x4 x1 = *reinterpret_cast<const f32x4*>(p + 4);
           float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
+          for (int k = 0; k < 8; ++k)  // a NaN may have all its bits in the half that is cut off
+            x[k] = x[k] == x[k] ? x[k] : __builtin_nanf("");
+#pragma unroll
           for (int t = 0; t < NT; ++t) {
             u32x4 w;
 #pragma unroll

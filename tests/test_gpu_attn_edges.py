@@ -122,6 +122,20 @@ def test_infinite_values(dev, dtype, rows, keys):
     assert bool(((rest - 1).abs() <= 2.0 ** -8 + 2.0 ** -15).all())
 
 
+@pytest.mark.parametrize("bits", [0x7f800001, 0x7f80ffff, 0xff800001, 0x7fc00000])
+def test_every_nan_of_an_fp32_query_is_nan(dev, bits):
+    """Also one whose payload lies in the low half, over keys that all have one sign."""
+    import beam_search_step_amd as bs
+    for sign in (0, 0x80):
+        cache, _, _ = make_cache(dev, 2, 16, 1, 64, 3)
+        cache.k.fill_(0x38 | sign)                  # +-1
+        q = torch.ones(1, 1, 64)
+        q.view(torch.int32)[0, 0, 5] = bits - (1 << 32) if bits >> 31 else bits
+        assert bool(torch.isnan(q[0, 0, 5]))
+        out = bs.CacheAttention(1, 1, 1, 1, 64, 16, 2, dtype="f32")(q.to(dev), cache, i32([[0, 1]], dev), i32([20], dev))
+        assert bool(torch.isnan(out).all()), (hex(bits), sign)
+
+
 # --- scales of blocks that are not read -----------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
