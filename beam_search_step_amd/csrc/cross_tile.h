@@ -19,12 +19,15 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 //                 register 4 b + r is value 32 j + 8 b + 4 hh + r
 // The next tile's loads go straight to LDS while this one is used, so they take no
 // registers, no instructions to turn V, and no writes. 8 items of 1024 rows over
-// 2048 keys, 32 heads of 128: 320 us, 860 TFLOP/s; through registers, V turned on
-// the way, 345. The matrix units are busy 42 % of the time: between two barriers
-// (4200 cycles, 1024 of them a wave's matrix instructions) the waves meet at the
-// loads (32 KB at the 64 bytes a cycle that a CU takes in), the exponentials, and
-// the barrier. Tried and no better: scores of the next tile during this one's
-// exponentials, two tiles between barriers, priorities for the matrix phases.
+// 2048 keys, 32 heads of 128: 390 us, 705 TFLOP/s, or 1060 of matrix instructions, the
+// second product being done in two terms. In one term (2^-8 of a probability instead
+// of 2^-15) it is 293 us, but a query would then be answered less exactly beside many
+// rows than beside few, where the other kernels keep two. Between two barriers the
+// waves meet at the loads (32 KB at the 64 bytes a cycle that a CU takes in), the
+// exponentials, and the barrier. Tried and no better: each 16 keys' exponentials right
+// before their products, both terms' products side by side over the values' tiles;
+// with one term, scores of the next tile during this one's exponentials, two tiles
+// between barriers, priorities for the matrix phases.
 template <int DP>
 struct TileLds {
   static constexpr int KT = 8192 / DP;   // keys of a tile: 16 KB of K and of V
@@ -183,10 +186,8 @@ __global__ __launch_bounds__(NW * 64, DP == 256 ? 1 : 2) void a3_tile(CrossArgs 
   for (int j = 0; j < VD; ++j)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
-  float m = -kInf, l = 0.0f;
+  float m = -kInf, l = 0.0f, l1 = 0.0f;  // l, l1: sums of every other key
   const float c = a.q.c;
-  bf16x2 ones;
-  ones.x = ones.y = (__bf16)1.0f;
 
   // this lane's places in a tile: K's row x, chunk 2 s + hh; V's row 4 hh + y / 4 of
   // 16 kk + 8 b .., values 32 j + 16 (x / 16) + 4 (y % 4) .., y the lane in its 16
@@ -251,6 +252,7 @@ __global__ __launch_bounds__(NW * 64, DP == 256 ? 1 : 2) void a3_tile(CrossArgs 
       const float mn = fmaxf(m, top);
       const float alpha = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
       l *= alpha;
+      l1 *= alpha;
 #pragma unroll
       for (int j = 0; j < VD; ++j)
 #pragma unroll
@@ -258,24 +260,25 @@ __global__ __launch_bounds__(NW * 64, DP == 256 ? 1 : 2) void a3_tile(CrossArgs 
       m = mn;
     }
     const float ref = m == -kInf ? 0.0f : m;
-    // the sum is of the rounded probabilities, those that the product uses
-    bf16x8 pf[2 * NT];
+    // probabilities in two bf16 terms, as everywhere for bf16 outputs (2^-15); values
+    // may be infinite, so the second is never zero (split_p)
+    bf16x8 pf[2 * NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2) {
-        u32x4 w;
+        u32x4 hi, lo;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float p0 = __builtin_amdgcn_exp2f(fmaf(st[t][8 * k2 + 2 * k], c, -ref));
           const float p1 = __builtin_amdgcn_exp2f(fmaf(st[t][8 * k2 + 2 * k + 1], c, -ref));
-          bf16x2 pair;
-          pair.x = (__bf16)p0;
-          pair.y = (__bf16)p1;
-          l = __builtin_amdgcn_fdot2_f32_bf16(pair, ones, l, false);
-          w[k] = __builtin_bit_cast(uint32_t, pair);
+          l += p0;
+          l1 += p1;
+          hi[k] = high_halves(p0, p1);
+          lo[k] = high_halves(fmaf(p0, kRestUp, -trunc_bf16(p0)), fmaf(p1, kRestUp, -trunc_bf16(p1)));
         }
-        pf[2 * t + k2] = as_bf16x8(w);
+        pf[2 * t + k2][0] = as_bf16x8(hi);
+        pf[2 * t + k2][1] = as_bf16x8(lo);
       }
 #pragma unroll
     for (int kk = 0; kk < 2 * NT; ++kk)
@@ -286,13 +289,15 @@ __global__ __launch_bounds__(NW * 64, DP == 256 ? 1 : 2) void a3_tile(CrossArgs 
         const s16x4 lo = read_transposed(p), hi = read_transposed(p + 8 * DP * 2);
         const bf16x8 w = __builtin_bit_cast(
             bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, pf[kk], acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, pf[kk][0], acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, pf[kk][1], acc[j], 0, 0, 0);
       }
     if (more) tile_ready<DP, NW>(a.q.D, seen, lds.k[buf ^ 1], lds.v[buf ^ 1]);
     __syncthreads();
   }
 
   {
+    l += l1;
     auto sw = __builtin_amdgcn_permlane32_swap(as_u(l), as_u(l), false, false);
     l = as_f(sw[0]) + as_f(sw[1]);
   }

@@ -4,6 +4,7 @@ References and tolerances are those of tests/attn_ref.py; cross attention is hel
 the bound of two-term probabilities at every number of columns."""
 import math
 import os
+import random
 
 import pytest
 
@@ -27,6 +28,56 @@ def dev():
     torch.set_num_threads(min(threads, len(os.sched_getaffinity(0))))
     yield torch.device("cuda", 0)
     torch.set_num_threads(threads)
+
+
+def cross_want(q, k, v, lens, mask, scale, dtype):
+    """ref.cross_attention with the two-term bound, whatever the number of columns."""
+    b, rows, hq, d = q.shape
+    hk = k.shape[2]
+    grp = hq // hk
+    o, tol = torch.zeros_like(q), torch.zeros_like(q)
+    for i in range(b):
+        at = torch.arange(k.shape[1] if lens is None else max(0, min(int(lens[i]), k.shape[1])))
+        if mask is not None:
+            at = at[mask[i, at] != 0]
+        for h in range(hk):
+            sl = slice(h * grp, (h + 1) * grp)
+            x = q[i, :, sl].reshape(-1, d)
+            y, t = ref.attend(x, k[i, at, h], v[i, at, h], torch.ones(x.shape[0], at.numel(), dtype=torch.bool),
+                              scale, dtype, 1)
+            o[i, :, sl], tol[i, :, sl] = y.view(rows, grp, d), t.view(rows, grp, d)
+    return o, tol
+
+
+def cross_case(dev, batch, rows, heads, kv_heads, dim, keys, dtype, seed, mask=False):
+    import beam_search_step_amd as bs
+    rng = random.Random(seed)
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn((batch, rows, heads, dim), generator=g).to(DT[dtype])
+    k, v = [torch.randn((batch, keys, kv_heads, dim), generator=g).to(DT[dtype]) for _ in range(2)]
+    ln = [keys] + [rng.randint(0, keys) for _ in range(batch - 1)]
+    mk = (torch.rand((batch, keys), generator=g) < 0.6).to(torch.uint8) if mask else None
+    kd, vd = k.clone(), v.clone()                 # what is not seen holds NaN and infinities
+    for b in range(batch):
+        kd[b, ln[b]:], vd[b, ln[b]:] = math.nan, math.inf
+        if mask:
+            kd[b, mk[b] == 0], vd[b, mk[b] == 0] = math.inf, math.nan
+    say("cross", batch, rows, heads, kv_heads, dim, keys, dtype, mask)
+    out = bs.CrossAttention(batch, rows, heads, kv_heads, dim, keys, dtype)(
+        q.to(dev), kd.to(dev), vd.to(dev), lens=i32(ln, dev), mask=None if mk is None else mk.to(dev))
+    want, tol = cross_want(q.double(), k.double(), v.double(), ln, mk, dim ** -0.5, dtype)
+    ref.check(out, want, tol, "cross attention")
+
+
+# --- one bound at every number of columns ----------------------------------------
+
+@pytest.mark.parametrize("case", [
+    (2, 20, 2, 2, 128, 300), (1, 64, 1, 1, 128, 1403), (3, 9, 8, 2, 64, 200), (1, 150, 4, 2, 64, 700),
+    (2, 300, 2, 1, 128, 513), (1, 5, 7, 1, 96, 77), (32, 260, 8, 8, 64, 130), (1, 40, 1, 1, 256, 900),
+])
+def test_probabilities_keep_their_bits_at_every_number_of_columns(dev, case):
+    """The same bound for 5 and for hundreds of columns: fp32 arithmetic, rounded once."""
+    cross_case(dev, *case, "bf16", seed=sum(case), mask=case[1] % 2 == 0)
 
 
 # --- infinite scores and values -----------------------------------------------------
