@@ -9,7 +9,7 @@ import random
 import pytest
 
 import attn_ref as ref
-from test_gpu_attn import i32, make_cache, say
+from test_gpu_attn import cache_case, i32, make_cache, say
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +206,24 @@ def test_scales_of_blocks_that_no_table_names(dev, dtype, block, scale):
     out = bs.CacheAttention(3, 1, 4, 2, dim, block, mb, dtype=dtype)(q.to(dev), cache, i32(table, dev), i32(lens, dev))
     want, tol = ref.cache_attention(q.double(), *vals, table, lens, None, None, 1, 1, dim ** -0.5, dtype)
     ref.check(out, want, tol, "scales")
+
+
+# --- head sizes above 128 ---------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", [False, True])
+@pytest.mark.parametrize("case", [
+    (2, 40, 1, 1, 256, 129), (2, 200, 2, 2, 256, 77), (1, 60, 3, 1, 144, 333), (2, 70, 2, 1, 208, 100),
+    (1, 130, 1, 1, 240, 1000), (1, 36, 2, 2, 256, 3001), (3, 5, 8, 2, 144, 50), (2, 1, 16, 1, 208, 700),
+])
+def test_cross_attention_of_heads_above_128(dev, case, mask, dtype):
+    cross_case(dev, *case, dtype, seed=sum(case), mask=mask)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [
+    (2, 3, 1, 4, 2, 256, 16, 90, 40), (1, 2, 5, 4, 1, 208, 32, 70, 33), (2, 1, 8, 2, 2, 256, 16, 0, 300),
+    (1, 16, 1, 4, 2, 144, 16, 520, 30), (1, 1, 1, 1, 1, 240, 48, 0, 1300), (1, 8, 3, 6, 2, 256, 32, 200, 50),
+])
+def test_cache_attention_of_heads_above_128(dev, case, dtype):
+    cache_case(dev, *case, dtype, seed=sum(case))
