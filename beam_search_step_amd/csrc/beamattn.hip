@@ -95,7 +95,9 @@ bool aligned(const void* p, int n) { return ((uintptr_t)p % n) == 0; }
 bool dtype_ok(int t) { return t == BS_F32 || t == BS_BF16; }
 int elem_size(int t) { return t == BS_F32 ? 4 : 2; }
 bool head_dim_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
-bool scale_ok(double s) { return s > 0 && s < 1e30; }
+// as a normal fp32 number, log2(e) times it too: a zero would make NaN of the -inf of
+// a key that is not seen
+bool scale_ok(double s) { return s >= 1e-37 && s < 1e30; }
 
 constexpr int64_t kMaxPosStride = (int64_t)1 << 26;   // lane offsets of a step stay below 2^31
 constexpr int64_t kTilePosStride = (int64_t)1 << 24;  // and those of a3_tile's 128 keys

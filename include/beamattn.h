@@ -150,7 +150,7 @@ typedef struct {
                                   size below 2^30                               */
     int32_t max_prompt_blocks; /* entries of an item's prompt table; 0: none    */
     int32_t dtype;             /* of queries and outputs                        */
-    double scale;              /* > 0, finite                                   */
+    double scale;              /* from 1e-37, below 1e30                        */
 } bs_cache_attn_config;
 
 typedef struct bs_cache_attn_state bs_cache_attn_state;
@@ -194,7 +194,7 @@ typedef struct {
     int32_t head_dim;  /* a multiple of 16 up to 256                            */
     int32_t max_keys;  /* the most keys of an item, >= 1, below 2^30            */
     int32_t dtype;     /* of queries, keys, values and outputs                  */
-    double scale;      /* > 0, finite                                           */
+    double scale;      /* from 1e-37, below 1e30                                */
 } bs_cross_attn_config;
 
 typedef struct bs_cross_attn_state bs_cross_attn_state;
