@@ -150,9 +150,11 @@ def _gpu_device(stream):
     return stream.device if stream is not None else torch.device("cuda", torch.cuda.current_device())
 
 
-def _table_arg(table, rows: int, device):
+def _table_arg(table, rows: int, device, block_size: int):
     """(address, entries per row) of a block table: a tensor, or a PagedKV's own."""
     if isinstance(table, _bs.PagedKV):
+        if not table.h:  # its device memory is freed
+            raise ValueError("table: the PagedKV is closed")
         if table.search.B * table.search.W != rows:
             raise ValueError(f"table: {table.search.B * table.search.W} rows, {rows} needed")
         if table.search.device != device:
@@ -214,7 +216,7 @@ class BlockMap:
             if self._table is None:
                 self._table = torch.empty((self.n, self.max_blocks), dtype=i32, device=dev)
             table = self._table
-        at, width = _table_arg(table, self.n, dev)
+        at, width = _table_arg(table, self.n, dev, self.block_size)
         if width != self.max_blocks:
             raise ValueError(f"table: {width} entries per row, expected {self.max_blocks}")
         # an empty list is a list still: any address will do
@@ -348,7 +350,7 @@ class CacheAttention:
         stride = _head_rows(q, "q", (self._n,), c.heads, c.head_dim)
         if cache.device != dev:
             raise ValueError(f"cache: on {cache.device}, expected {dev}")
-        at, width = _table_arg(table, self._rows, dev)
+        at, width = _table_arg(table, self._rows, dev, c.block_size)
         if width < c.max_blocks:
             raise ValueError(f"table: {width} entries per row, {c.max_blocks} needed")
         _need(lens, "lens", dev, self._i32, (self._rows,))

@@ -18,3 +18,26 @@ def test_scales_that_fp32_does_not_hold_are_refused(scale):
                         (L.bs_cross_attn_create, attn.bs_cross_attn_config(1, 1, 1, 1, 64, 8, 1, scale))):
         assert create(ctypes.addressof(cfg), None, ctypes.addressof(h)) == bs.BS_EINVAL
         assert h.value is None
+
+
+def paged_kv(device, rows=4, block=16, entries=3, h=None):
+    """A PagedKV as the binding sees it, without a device behind it."""
+    from types import SimpleNamespace
+    p = bs.PagedKV.__new__(bs.PagedKV)
+    p.search = SimpleNamespace(B=rows // 2, W=2, device=device)
+    p.block_size, p.max_blocks, p._addr, p.h = block, entries, 1 << 20, h
+    return p
+
+
+def test_the_table_of_a_closed_paged_cache_is_refused():
+    """Its memory is freed."""
+    torch = pytest.importorskip("torch")
+    dev = torch.device("meta")
+    p = paged_kv(dev)
+    with pytest.raises(ValueError, match="closed"):
+        attn._table_arg(p, 4, dev, 16)
+    p.h = 1
+    try:
+        assert attn._table_arg(p, 4, dev, 16) == (1 << 20, 3)
+    finally:
+        p.h = None
