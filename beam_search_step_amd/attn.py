@@ -155,6 +155,8 @@ def _table_arg(table, rows: int, device, block_size: int):
     if isinstance(table, _bs.PagedKV):
         if not table.h:  # its device memory is freed
             raise ValueError("table: the PagedKV is closed")
+        if table.block_size != block_size:
+            raise ValueError(f"table: blocks of {table.block_size} positions, {block_size} needed")
         if table.search.B * table.search.W != rows:
             raise ValueError(f"table: {table.search.B * table.search.W} rows, {rows} needed")
         if table.search.device != device:

@@ -41,3 +41,14 @@ def test_the_table_of_a_closed_paged_cache_is_refused():
         assert attn._table_arg(p, 4, dev, 16) == (1 << 20, 3)
     finally:
         p.h = None
+
+
+def test_the_table_of_a_paged_cache_of_another_block_size_is_refused():
+    torch = pytest.importorskip("torch")
+    dev = torch.device("meta")
+    p = paged_kv(dev, h=1)
+    try:
+        with pytest.raises(ValueError, match="blocks of 16"):
+            attn._table_arg(p, 4, dev, 8)
+    finally:
+        p.h = None
