@@ -504,6 +504,9 @@ class PagedKV:
 
     def reorder_quant(self, caches, gen_len: int):
         """The reorder of layers held in 8 bits (QuantCache): data and scales."""
+        for c in caches:
+            if c.device != self.search.device:
+                raise ValueError(f"cache: on {c.device}, expected {self.search.device}")
         bs_kvq_reorder(self.h, caches, gen_len)
 
     def status(self):

@@ -150,6 +150,11 @@ def _gpu_device(stream):
     return stream.device if stream is not None else torch.device("cuda", torch.cuda.current_device())
 
 
+def _check_stream(stream, device) -> None:
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
+
+
 def _table_arg(table, rows: int, device, block_size: int):
     """(address, entries per row) of a block table: a tensor, or a PagedKV's own."""
     if isinstance(table, _bs.PagedKV):
@@ -253,6 +258,7 @@ class QuantCache:
         if k.stride(3) != 1 or (h > 1 and k.stride(2) != d):
             raise ValueError("k, v: the heads of a position must be contiguous")
         self.device = k.device
+        _check_stream(stream, self.device)
         _need(v, "v", self.device, k.dtype)
         _need(k_scale, "k_scale", self.device, torch.float32, (n, h))
         _need(v_scale, "v_scale", self.device, torch.float32, (n, h))

@@ -52,3 +52,15 @@ def test_the_table_of_a_paged_cache_of_another_block_size_is_refused():
             attn._table_arg(p, 4, dev, 8)
     finally:
         p.h = None
+
+
+def test_caches_and_streams_of_another_device_are_refused():
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    p = paged_kv(torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="cuda:1"):
+        p.reorder_quant([SimpleNamespace(device=torch.device("cuda", d)) for d in (0, 1)], 1)
+    attn._check_stream(None, torch.device("cuda", 0))
+    attn._check_stream(SimpleNamespace(device=torch.device("cuda", 0)), torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="cuda:1"):
+        attn._check_stream(SimpleNamespace(device=torch.device("cuda", 1)), torch.device("cuda", 0))
