@@ -101,6 +101,16 @@ def _torch_dtypes():
     return {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
+_MOST = 2 ** 31 - 1  # the largest count that the library takes
+
+
+def _int32(**values) -> None:
+    """Refuses values that ctypes would cut to 32 bits."""
+    for name, v in values.items():
+        if not -_MOST <= v <= _MOST:
+            raise ValueError(f"{name}: {v} is no int32")
+
+
 def _need(t, what: str, device, dtype, shape=None):
     """A tensor on the device, of the type and, when a shape is given, contiguous and of it."""
     if t.device == device and t.dtype is dtype and (
@@ -169,7 +179,7 @@ def _table_arg(table, rows: int, device, block_size: int):
         return table._addr, table.max_blocks
     _need(table, "table", device, _t().int32)
     shape = table.shape
-    if len(shape) != 2 or shape[0] != rows or not table.is_contiguous():
+    if len(shape) != 2 or shape[0] != rows or shape[1] > _MOST or not table.is_contiguous():
         raise ValueError(f"table: a contiguous tensor [{rows}, entries] is needed, not "
                          f"{list(shape)}")
     return table.data_ptr(), shape[1]
@@ -217,6 +227,8 @@ class BlockMap:
             if isinstance(table, _bs.PagedKV):
                 raise ValueError("a PagedKV's table is only read: no free_blocks")
             n_free = free_blocks.numel()
+            if n_free > _MOST:
+                raise ValueError(f"free_blocks: {n_free} entries, at most {_MOST}")
         if table is None:
             if starts is not None or free_blocks is None:
                 raise ValueError("table: needed with starts, and without free_blocks")
@@ -251,6 +263,7 @@ class QuantCache:
             raise ValueError("k, v: two pools [n_blocks, block_size, kv_heads, head_dim] of one "
                              "shape, type and strides are needed")
         n, bs, h, d = k.shape
+        _int32(n_blocks=n, block_size=bs, kv_heads=h, head_dim=d)
         if not k.is_cuda:
             raise ValueError("k: a GPU tensor is needed")
         if k.dtype not in (torch.uint8, torch.float8_e4m3fn):
@@ -293,8 +306,9 @@ class QuantCache:
         if _head_rows(v, "v", (n,), self.heads, self.head_dim) != stride:
             raise ValueError("k, v: rows must be equally spaced")
         _need(slots, "slots", self.device, torch.int32)
-        if slots.dim() != 1 or slots.shape[0] < n or not slots.is_contiguous():
-            raise ValueError(f"slots: a contiguous list of at least {n} is needed")
+        if slots.dim() != 1 or slots.shape[0] < n or n > _MOST or not slots.is_contiguous():
+            raise ValueError(f"slots: a contiguous list of at least {n} (and {n} at most {_MOST}) "
+                             "is needed")
         _bs._check(_on_device(self.device, self.stream, self._write, self._ref,
                               _bs.BS_F32 if f32 else _bs.BS_BF16, k.data_ptr(), v.data_ptr(),
                               stride, slots.data_ptr(), n), "bs_kvq_write")
@@ -302,8 +316,8 @@ class QuantCache:
     def read(self, slots, dtype="f32"):
         torch = _t()
         _need(slots, "slots", self.device, torch.int32)
-        if slots.dim() != 1 or not slots.is_contiguous():
-            raise ValueError("slots: a contiguous list is needed")
+        if slots.dim() != 1 or slots.shape[0] > _MOST or not slots.is_contiguous():
+            raise ValueError(f"slots: a contiguous list of at most {_MOST} is needed")
         n = slots.shape[0]
         shape = (2, n, self.heads, self.head_dim)
         if self.stream is None:
@@ -336,6 +350,9 @@ class CacheAttention:
     def __init__(self, batch, rows, heads, kv_heads, head_dim, block_size, max_blocks,
                  max_prompt_blocks=0, q_len=1, dtype="bf16", scale=None, stream=None):
         torch = _t()
+        _int32(batch=batch, rows=rows, q_len=q_len, heads=heads, kv_heads=kv_heads,
+               head_dim=head_dim, block_size=block_size, max_blocks=max_blocks,
+               max_prompt_blocks=max_prompt_blocks)
         cfg = bs_cache_attn_config(batch, rows, q_len, heads, kv_heads, head_dim, block_size,
                                    max_blocks, max_prompt_blocks, _bs.DTYPES[dtype],
                                    head_dim ** -0.5 if scale is None else scale)
@@ -405,6 +422,8 @@ class CrossAttention:
     def __init__(self, batch, max_rows, heads, kv_heads, head_dim, max_keys, dtype="bf16",
                  scale=None, stream=None):
         torch = _t()
+        _int32(batch=batch, max_rows=max_rows, heads=heads, kv_heads=kv_heads, head_dim=head_dim,
+               max_keys=max_keys)
         cfg = bs_cross_attn_config(batch, max_rows, heads, kv_heads, head_dim, max_keys,
                                    _bs.DTYPES[dtype], head_dim ** -0.5 if scale is None else scale)
         self.cfg, self._lib = cfg, attn_library()

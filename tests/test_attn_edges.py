@@ -64,3 +64,33 @@ def test_caches_and_streams_of_another_device_are_refused():
     attn._check_stream(SimpleNamespace(device=torch.device("cuda", 0)), torch.device("cuda", 0))
     with pytest.raises(ValueError, match="cuda:1"):
         attn._check_stream(SimpleNamespace(device=torch.device("cuda", 1)), torch.device("cuda", 0))
+
+
+def test_counts_that_an_int32_does_not_hold_are_refused():
+    """They would reach the library cut to 32 bits."""
+    torch = pytest.importorskip("torch")
+    dev = torch.device("meta")
+    big = (1 << 32) + 8
+    m = bs.BlockMap.__new__(bs.BlockMap)
+    m.n, m.block_size, m.max_blocks, m.device, m._table = 4, 16, 8, dev, None
+    lens = torch.zeros(4, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError, match="free_blocks"):
+        m(lens, torch.empty(big, dtype=torch.int32, device=dev))
+    with pytest.raises(ValueError, match="table"):
+        attn._table_arg(torch.empty((1, big), dtype=torch.int32, device=dev), 1, dev, 16)
+    c = bs.QuantCache.__new__(bs.QuantCache)
+    c.device, c.heads, c.head_dim, c.stream = dev, 1, 16, None
+    x, slots = torch.empty((big, 1, 16), dtype=torch.bfloat16, device=dev), torch.empty(big, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError, match="slots"):
+        c.write(x, x, slots)
+    with pytest.raises(ValueError, match="slots"):
+        c.read(slots)
+    for kw in (dict(batch=big), dict(rows=big), dict(heads=big), dict(max_blocks=big), dict(block_size=-big)):
+        a = dict(batch=1, rows=1, heads=1, kv_heads=1, head_dim=64, block_size=16, max_blocks=4)
+        a.update(kw)
+        with pytest.raises(ValueError, match="int32"):
+            bs.CacheAttention(**a)
+    with pytest.raises(ValueError, match="int32"):
+        bs.CrossAttention(1, 1, 1, 1, 64, big)
+    with pytest.raises(ValueError, match="int32"):
+        attn._int32(n_blocks=4, block_size=big)
