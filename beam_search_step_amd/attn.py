@@ -7,6 +7,7 @@ caller's tensors, whose sizes the library cannot see.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -165,6 +166,12 @@ def _check_stream(stream, device) -> None:
         raise ValueError(f"stream: on {stream.device}, expected {device}")
 
 
+def _memory_of(stream):
+    """Allocations (and fills) inside belong to the stream that was given to an object: its
+    kernels run there, and the allocator orders reuse by stream."""
+    return contextlib.nullcontext() if stream is None else _t().cuda.stream(stream)
+
+
 def _table_arg(table, rows: int, device, block_size: int):
     """(address, entries per row) of a block table: a tensor, or a PagedKV's own."""
     if isinstance(table, _bs.PagedKV):
@@ -206,9 +213,10 @@ class BlockMap:
         self.device = _gpu_device(stream)
         self.stream = stream
         kw = dict(dtype=torch.int32, device=self.device)
-        self.cu = torch.empty(n + 1, **kw)
-        self.slots = torch.empty(max_tokens, **kw)
-        self.used = torch.empty(1, **kw)
+        with _memory_of(stream):
+            self.cu = torch.empty(n + 1, **kw)
+            self.slots = torch.empty(max_tokens, **kw)
+            self.used = torch.empty(1, **kw)
         self._cu, self._used = self.cu.data_ptr(), self.used.data_ptr()
         self._slots = self.slots.data_ptr() or None
         self._table = None
@@ -233,7 +241,8 @@ class BlockMap:
             if starts is not None or free_blocks is None:
                 raise ValueError("table: needed with starts, and without free_blocks")
             if self._table is None:
-                self._table = torch.empty((self.n, self.max_blocks), dtype=i32, device=dev)
+                with _memory_of(self.stream):
+                    self._table = torch.empty((self.n, self.max_blocks), dtype=i32, device=dev)
             table = self._table
         at, width = _table_arg(table, self.n, dev, self.block_size)
         if width != self.max_blocks:
@@ -252,7 +261,8 @@ class QuantCache:
 
     k, v: uint8 or float8_e4m3fn [n_blocks, block_size, kv_heads, head_dim]
     (e4m3 bytes; blocks and positions may be strided); k_scale, v_scale: float32
-    [n_blocks, kv_heads]. ``QuantCache.empty(...)`` allocates them.
+    [n_blocks, kv_heads]. ``QuantCache.empty(...)`` allocates and fills them, on the
+    stream that it is given.
     ``write(k, v, slots)`` rounds new tokens into their slots, ``read(slots,
     dtype)`` returns what slots hold; both run on the given or current stream.
     """
@@ -290,9 +300,11 @@ class QuantCache:
     def empty(cls, n_blocks, block_size, kv_heads, head_dim, device=None, stream=None):
         torch = _t()
         kw = dict(device=device if device is not None else _gpu_device(stream))
-        pools = [torch.zeros((n_blocks, block_size, kv_heads, head_dim), dtype=torch.uint8, **kw)
-                 for _ in range(2)]
-        scales = [torch.ones((n_blocks, kv_heads), dtype=torch.float32, **kw) for _ in range(2)]
+        with _memory_of(stream):
+            pools = [torch.zeros((n_blocks, block_size, kv_heads, head_dim), dtype=torch.uint8,
+                                 **kw) for _ in range(2)]
+            scales = [torch.ones((n_blocks, kv_heads), dtype=torch.float32, **kw)
+                      for _ in range(2)]
         return cls(*pools, *scales, stream=stream)
 
     def write(self, k, v, slots) -> None:
@@ -363,8 +375,9 @@ class CacheAttention:
             ctypes.addressof(cfg), raw, ctypes.addressof(h))), "bs_cache_attn_create")
         self.h = h.value
         self._rows, self._n = batch * rows, batch * rows * q_len
-        self.out = torch.empty((self._n, heads, head_dim), dtype=_torch_dtypes()[dtype],
-                               device=self.device)
+        with _memory_of(stream):
+            self.out = torch.empty((self._n, heads, head_dim), dtype=_torch_dtypes()[dtype],
+                                   device=self.device)
         self._i32 = torch.int32
 
     def __call__(self, q, cache: QuantCache, table, lens, prompt_table=None, prompt_lens=None,
@@ -432,8 +445,9 @@ class CrossAttention:
         _bs._check(_on_device(self.device, stream, lambda raw: self._lib.bs_cross_attn_create(
             ctypes.addressof(cfg), raw, ctypes.addressof(h))), "bs_cross_attn_create")
         self.h = h.value
-        self._buf = torch.empty(batch * max_rows * heads * head_dim, dtype=_torch_dtypes()[dtype],
-                                device=self.device)
+        with _memory_of(stream):
+            self._buf = torch.empty(batch * max_rows * heads * head_dim,
+                                    dtype=_torch_dtypes()[dtype], device=self.device)
         self._i32, self._mask_types = torch.int32, (torch.uint8, torch.bool)
         self._outs = {}  # the views of _buf by their rows
         self._kv = bs_cross_kv()

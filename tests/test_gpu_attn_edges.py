@@ -227,3 +227,56 @@ def test_cross_attention_of_heads_above_128(dev, case, mask, dtype):
 ])
 def test_cache_attention_of_heads_above_128(dev, case, dtype):
     cache_case(dev, *case, dtype, seed=sum(case))
+
+
+# --- streams ----------------------------------------------------------------------------
+
+def stream_of(t):
+    """The raw stream whose pool a tensor's memory belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("no segment")
+
+
+def test_what_an_object_allocates_belongs_to_its_stream(dev):
+    """Otherwise the allocator may hand over memory that the current stream still uses,
+    and fills on the current stream may come after the first write."""
+    import beam_search_step_amd as bs
+    s = torch.cuda.Stream()
+    m = bs.BlockMap(2, 4, 3, 8, stream=s)
+    m(i32([3, 5], dev), i32([0, 1, 2, 3], dev))
+    c = bs.QuantCache.empty(6, 4, 2, 64, stream=s)
+    own = [m.cu, m.slots, m.used, m._table, c.k, c.v, c.k_scale, c.v_scale,
+           bs.CacheAttention(2, 1, 4, 2, 64, 4, 3, stream=s).out,
+           bs.CrossAttention(2, 3, 4, 2, 64, 9, stream=s)._buf]
+    torch.cuda.synchronize()
+    assert [stream_of(t) for t in own] == [s.cuda_stream] * len(own)
+
+
+def busy(n=40):
+    """Some tens of milliseconds of work on the current stream."""
+    x = torch.full((4096, 4096), 2.0 ** -12, device="cuda")
+    for _ in range(n):
+        x = x @ x
+    return x
+
+
+def test_a_cache_made_for_a_stream_while_the_current_one_is_busy(dev):
+    import beam_search_step_amd as bs
+    s = torch.cuda.Stream()
+    x = [torch.randn(8, 2, 64, generator=torch.Generator().manual_seed(i)).to(dev) for i in range(2)]
+    slots = i32(list(range(8)), dev)
+    torch.cuda.synchronize()
+    keep = busy()
+    c = bs.QuantCache.empty(3, 4, 2, 64, stream=s)
+    c.write(*x, slots)
+    first = c.read(slots)
+    s.synchronize()
+    first = [t.cpu() for t in first]
+    torch.cuda.synchronize()
+    again = [t.cpu() for t in c.read(slots)]
+    del keep
+    for t, a, b in zip(x, first, again):
+        assert torch.equal(a, b)
+        assert bool(((a - t.cpu()).abs() <= 2.0 ** -4 * t.cpu().abs() + 2.0 ** -9).all())
