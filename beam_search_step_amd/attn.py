@@ -172,6 +172,40 @@ def _memory_of(stream):
     return contextlib.nullcontext() if stream is None else _t().cuda.stream(stream)
 
 
+class _Handle:
+    """A handle of the library, whose calls are all on one stream: the one given, or the
+    current one of the time when it was made. In the second case a call under another
+    stream is kept in order with that: a caller who names no stream expects the current one's
+    order."""
+
+    h = None
+
+    def _create(self, fn, cfg, stream):
+        torch = _t()
+        self.device = _gpu_device(stream)
+        self._made_on = None if stream is not None else torch.cuda.current_stream(self.device)
+        self._raw = (self._made_on if stream is None else stream).cuda_stream
+        self._current = torch._C._cuda_getCurrentRawStream
+        h = ctypes.c_void_p()
+        _bs._check(_on_device(self.device, stream, lambda raw: fn(
+            ctypes.addressof(cfg), raw, ctypes.addressof(h))), fn.__name__)
+        self.h = h.value
+
+    def _call(self, fn, *args) -> int:
+        made = self._made_on
+        if made is None or self._current(self.device.index) == self._raw:
+            return fn(self.h, *args)
+        torch = _t()
+        now = torch.cuda.current_stream(self.device)
+        if self._raw == 0 and torch.cuda.is_current_stream_capturing():
+            raise ValueError("made under the null stream, which no capture can hold: make it "
+                             "under another stream, or give it one")
+        made.wait_stream(now)
+        status = fn(self.h, *args)
+        now.wait_stream(made)
+        return status
+
+
 def _table_arg(table, rows: int, device, block_size: int):
     """(address, entries per row) of a block table: a tensor, or a PagedKV's own."""
     if isinstance(table, _bs.PagedKV):
@@ -349,14 +383,15 @@ def bs_kvq_reorder(p: int, caches: Sequence[QuantCache], gen_len: int) -> None:
     _bs._check(attn_library().bs_kvq_reorder(p, arr, len(caches), gen_len), "bs_kvq_reorder")
 
 
-class CacheAttention:
+class CacheAttention(_Handle):
     """Attention of batch * rows rows over a QuantCache (bs_cache_attn).
 
     ``att(q, cache, table, lens, prompt_table=None, prompt_lens=None)`` with q
     [batch * rows * q_len, heads, head_dim] returns the output, of q's shape and
     type: the handle's own tensor, written again by the next call, or ``out``.
     ``table`` is a tensor [batch * rows, max_blocks] or a PagedKV. Every call runs
-    on the stream given here, or the one that was current when this was made.
+    on the stream given here; without one, on the stream that was current when this was
+    made, in order with the stream that is current at the call.
     """
 
     def __init__(self, batch, rows, heads, kv_heads, head_dim, block_size, max_blocks,
@@ -369,11 +404,7 @@ class CacheAttention:
                                    max_blocks, max_prompt_blocks, _bs.DTYPES[dtype],
                                    head_dim ** -0.5 if scale is None else scale)
         self.cfg, self._lib = cfg, attn_library()
-        self.device = _gpu_device(stream)
-        h = ctypes.c_void_p()
-        _bs._check(_on_device(self.device, stream, lambda raw: self._lib.bs_cache_attn_create(
-            ctypes.addressof(cfg), raw, ctypes.addressof(h))), "bs_cache_attn_create")
-        self.h = h.value
+        self._create(self._lib.bs_cache_attn_create, cfg, stream)
         self._rows, self._n = batch * rows, batch * rows * q_len
         with _memory_of(stream):
             self.out = torch.empty((self._n, heads, head_dim), dtype=_torch_dtypes()[dtype],
@@ -403,9 +434,8 @@ class CacheAttention:
             out = own
         else:
             _need(out, "out", dev, own.dtype, tuple(own.shape))
-        _bs._check(self._lib.bs_cache_attn(self.h, cache._ref, q.data_ptr(), stride, at, width,
-                                           lens.data_ptr(), pt, pl, out.data_ptr()),
-                   "bs_cache_attn")
+        _bs._check(self._call(self._lib.bs_cache_attn, cache._ref, q.data_ptr(), stride, at,
+                              width, lens.data_ptr(), pt, pl, out.data_ptr()), "bs_cache_attn")
         return out
 
     def close(self):
@@ -420,7 +450,7 @@ class CacheAttention:
             pass
 
 
-class CrossAttention:
+class CrossAttention(_Handle):
     """Attention of an item's rows to its encoder's states (bs_cross_attn).
 
     ``att(q, k, v, lens=None, mask=None)`` with q [batch, rows, heads, head_dim]
@@ -429,7 +459,8 @@ class CrossAttention:
     lens int32 [batch], mask uint8 or bool [batch, keys] (nonzero: seen) returns
     the output, of q's shape and type, contiguous: the handle's own memory,
     written again by the next call, or ``out``. Every call runs on the stream given
-    here, or the one that was current when this was made.
+    here; without one, on the stream that was current when this was made, in order with
+    the stream that is current at the call.
     """
 
     def __init__(self, batch, max_rows, heads, kv_heads, head_dim, max_keys, dtype="bf16",
@@ -440,11 +471,7 @@ class CrossAttention:
         cfg = bs_cross_attn_config(batch, max_rows, heads, kv_heads, head_dim, max_keys,
                                    _bs.DTYPES[dtype], head_dim ** -0.5 if scale is None else scale)
         self.cfg, self._lib = cfg, attn_library()
-        self.device = _gpu_device(stream)
-        h = ctypes.c_void_p()
-        _bs._check(_on_device(self.device, stream, lambda raw: self._lib.bs_cross_attn_create(
-            ctypes.addressof(cfg), raw, ctypes.addressof(h))), "bs_cross_attn_create")
-        self.h = h.value
+        self._create(self._lib.bs_cross_attn_create, cfg, stream)
         with _memory_of(stream):
             self._buf = torch.empty(batch * max_rows * heads * head_dim,
                                     dtype=_torch_dtypes()[dtype], device=self.device)
@@ -499,9 +526,9 @@ class CrossAttention:
                     self._buf[:c.batch * rows * c.heads * c.head_dim].view(q.shape)
         else:
             _need(out, "out", dev, dt, tuple(q.shape))
-        _bs._check(self._lib.bs_cross_attn(self.h, q.data_ptr() or None, stride, rows,
-                                           self._kv_ref, n, lp, mp, ms,
-                                           out.data_ptr() or None), "bs_cross_attn")
+        _bs._check(self._call(self._lib.bs_cross_attn, q.data_ptr() or None, stride, rows,
+                              self._kv_ref, n, lp, mp, ms, out.data_ptr() or None),
+                   "bs_cross_attn")
         return out
 
     def close(self):

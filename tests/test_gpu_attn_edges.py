@@ -280,3 +280,66 @@ def test_a_cache_made_for_a_stream_while_the_current_one_is_busy(dev):
     for t, a, b in zip(x, first, again):
         assert torch.equal(a, b)
         assert bool(((a - t.cpu()).abs() <= 2.0 ** -4 * t.cpu().abs() + 2.0 ** -9).all())
+
+
+def attentions(dev):
+    """Two handles and a call of both on given inputs."""
+    import beam_search_step_amd as bs
+    cache, _, _ = make_cache(dev, 4, 16, 2, 64, 7)
+    att, cross = bs.CacheAttention(2, 1, 4, 2, 64, 16, 2), bs.CrossAttention(2, 1, 4, 2, 64, 50)
+    table, lens = i32([[0, 1], [2, 3]], dev), i32([20, 32], dev)
+    torch.cuda.synchronize()
+    return lambda q, k, v: (att(q, cache, table, lens), cross(q.view(2, 1, 4, 64), k, v))
+
+
+def attention_inputs(dev, seed):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    return [torch.randn(s, generator=g, device=dev).bfloat16() for s in ((2, 4, 64), (2, 50, 2, 64), (2, 50, 2, 64))]
+
+
+def test_handles_made_under_another_stream_keep_in_order_with_the_current_one(dev):
+    """Without a stream of their own they wait for what the current stream made, and it
+    waits for them."""
+    call = attentions(dev)
+    s = torch.cuda.Stream()
+    data = [attention_inputs(dev, i) for i in range(4)]
+    want = []
+    for d in data:
+        want.append([o.clone() for o in call(*d)])
+    ins = [torch.zeros_like(x) for x in data[0]]
+    torch.cuda.synchronize()
+    got = []
+    with torch.cuda.stream(s):
+        keep = busy()
+        for d in data:
+            for x, y in zip(ins, d):
+                x.copy_(y)
+            got.append([o.clone() for o in call(*ins)])
+    torch.cuda.synchronize()
+    del keep
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_handles_made_under_another_stream_and_captured(dev):
+    """Their stream joins the capture; the null stream cannot, and is refused."""
+    default, a, b = attentions(dev), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(a):
+        call = attentions(dev)
+    ins = attention_inputs(dev, 0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=b):
+        with pytest.raises(ValueError, match="capture"):
+            default(*ins)
+        outs = call(*ins)
+    for i in range(1, 5):
+        for x, y in zip(ins, attention_inputs(dev, i)):
+            x.copy_(y)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        want = default(*ins)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), f"replay {i}"
