@@ -343,3 +343,31 @@ def test_handles_made_under_another_stream_and_captured(dev):
         want = default(*ins)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), f"replay {i}"
+
+
+
+def test_maps_and_caches_without_a_stream_follow_the_current_one(dev):
+    """Their memory may be freed while another stream still uses it: that stream is
+    recorded."""
+    import beam_search_step_amd as bs
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        m, c = bs.BlockMap(2, 4, 3, 8), bs.QuantCache.empty(6, 4, 2, 64)
+        x = torch.randn(8, 2, 64, device=dev)
+        lens, free = i32([3, 5], dev), i32([4, 1, 2, 3], dev)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            keep = busy()
+            table, slots, cu, used = [t.clone() for t in m(lens, free)]
+            c.write(x, x, m.slots)
+            k, v = c.read(slots)
+        at = [m._table.data_ptr(), c.k.data_ptr()]
+        del m, c
+        other = [torch.full((2, 3), 9, dtype=torch.int32, device=dev), torch.full((6, 4, 2, 64), 77, dtype=torch.uint8, device=dev)]
+        pending = not s.query()
+        say("still busy:", pending)
+        torch.cuda.synchronize()
+        assert not pending or at[0] != other[0].data_ptr() and at[1] != other[1].data_ptr(), "memory in use was handed over"
+        assert table.tolist() == [[4, -1, -1], [1, 2, -1]] and cu.tolist() == [0, 3, 8]
+        assert bool(((k - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -9).all()) and torch.equal(k, v)
+        del keep
