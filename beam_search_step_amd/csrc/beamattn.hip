@@ -163,19 +163,24 @@ int choose_waves(int64_t pairs, int64_t keys, bool one_kind) {
 
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-// 16-column tiles of a wave of a2_cross. Two where keys are worth reading once for
-// both and registers hold them without spilling: 32 columns of 14 items, 8 kv heads
-// of 64 and 1403 bf16 keys are 19 us, one tile at a time 23; 4096 columns of 512 fp32
-// keys 388 us against 575 and with four tiles 461.
+// The most 16-column tiles of a wave of a2_cross. Two where keys are worth reading
+// once for both and registers hold them without spilling: 32 columns of 14 items, 8 kv
+// heads of 64 and 1403 bf16 keys are 19 us, one tile at a time 23; 4096 columns of 512
+// fp32 keys 388 us against 575 and with four tiles 461.
 template <int DP, typename T>
 constexpr int cross_most() {
   return sizeof(T) == 2 ? (DP == 64 ? 2 : 1) : DP <= 128 ? 2 : 1;
 }
-// fp32 heads of 128: 56 columns of 1403 keys are 93 us one tile at a time (two: 116
-// where groups were dealt over the XCDs, one 110), 4096 columns of 512 keys 1170 and 1006
+// The tiles of a call, never more than that. fp32 heads of 128: 56 columns of 1403 keys
+// are 93 us one tile at a time (two: 116 where groups were dealt over the XCDs, one
+// 110), 4096 columns of 512 keys 1170 and 1006
 int cross_tiles(int64_t cols, int dp, int dtype) {
-  if (cols <= 16 || dp == 256) return 1;
-  return dp == 64 || (dtype == BS_F32 && cols > 64) ? 2 : 1;
+  if (cols <= 16 || (dtype == BS_F32 && dp == 128 && cols <= 64)) return 1;
+  if (dtype == BS_F32)
+    return dp == 64 ? cross_most<64, float>() : dp == 128 ? cross_most<128, float>()
+                                                           : cross_most<256, float>();
+  return dp == 64 ? cross_most<64, uint16_t>() : dp == 128 ? cross_most<128, uint16_t>()
+                                                            : cross_most<256, uint16_t>();
 }
 
 QueryArgs query_args(const void* q, int64_t q_stride, int heads, int kv_heads, int D, double scale,
@@ -604,8 +609,10 @@ int bs_cross_attn_create(const bs_cross_attn_config* cfg, void* hip_stream,
     free(h);
     return BS_EDEVICE;
   }
-  // partials of a launch that splits its keys: kWantGroups workgroups of up to
-  // 64 columns, twice over, and never more than every unit in kMaxSplits
+  // The partials that a call may use: every query and head in kMaxSplits, but at most
+  // 98,304 of them (50 MB at 128 values). A call of more than half as many queries and
+  // heads is not split, and one between gets the splits that fit, fewer than
+  // choose_splits may ask for.
   const int64_t all = (int64_t)c.batch * c.max_rows * c.heads * kMaxSplits;
   const int64_t want = (int64_t)kWantGroups * 128;
   h->units = all < want ? all : want;
