@@ -225,7 +225,7 @@ __global__ __launch_bounds__(NW * 64, (cache_waves<DP, NW, NT, UNI>())) void a1_
   const int head0 = h * a.q.group;
 
   const int len = min(max(s.lens[unit], 0), s.mb * a.bs);
-  // the keys of this split: 128 (a step of each wave) times a whole number
+  // the keys of this split: a step of each wave, times a whole number
   int per = (len + s.splits - 1) / s.splits;
   per = (per + NW * kStep - 1) / (NW * kStep) * (NW * kStep);
   const int begin = min((int64_t)sp * per, (int64_t)len), end = min(begin + per, len);

@@ -371,3 +371,57 @@ def test_maps_and_caches_without_a_stream_follow_the_current_one(dev):
         assert table.tolist() == [[4, -1, -1], [1, 2, -1]] and cu.tolist() == [0, 3, 8]
         assert bool(((k - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -9).all()) and torch.equal(k, v)
         del keep
+
+
+# --- handles wider than their calls ---------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch, rows, q_len, heads, kv_heads, dim, block, prompt", [
+    (2, 3, 1, 4, 2, 64, 16, 40), (1, 2, 4, 8, 2, 128, 24, 100), (3, 1, 1, 2, 2, 256, 32, 33), (16, 16, 1, 8, 8, 64, 16, 20),
+])
+def test_cache_attention_of_a_handle_much_wider_than_its_lengths(dev, dtype, batch, rows, q_len, heads, kv_heads, dim,
+                                                                 block, prompt):
+    """Tables of thousands of entries (wider than the handle asks for) of which few are
+    used, queries inside wider rows, then the same handle without a prompt and with
+    nothing at all."""
+    import beam_search_step_amd as bs
+    rng = random.Random(batch * dim)
+    R, mb, pmb = batch * rows, 700, 900
+    used, pused = -(-30 // block), -(-prompt // block)
+    n = R * used + batch * pused
+    cache, vals, _ = make_cache(dev, n, block, kv_heads, dim, 4)
+    ids = rng.sample(range(n), n)
+    table = [[ids.pop() for _ in range(used)] + [-1] * (mb + 5 - used) for _ in range(R)]
+    ptable = [[ids.pop() for _ in range(pused)] + [-1] * (pmb - pused) for _ in range(batch)]
+    lens, plens = [rng.randint(0, 30) for _ in range(R)], [rng.randint(0, prompt) for _ in range(batch)]
+    wide = torch.randn((R * q_len, 3 * heads, dim), generator=torch.Generator().manual_seed(6)).to(DT[dtype])
+    q = wide[:, heads:2 * heads]
+    say("wide handle", batch, rows, q_len, heads, dim, block, dtype)
+    att = bs.CacheAttention(batch, rows, heads, kv_heads, dim, block, mb, pmb, q_len, dtype)
+    td, pd, qd = i32(table, dev), i32(ptable, dev), wide.to(dev)[:, heads:2 * heads]
+    for p in (True, False):
+        kw = dict(prompt_table=pd, prompt_lens=i32(plens, dev)) if p else {}
+        out = att(qd, cache, td, i32(lens, dev), **kw)
+        want, tol = ref.cache_attention(q.double(), *vals, table, lens, ptable if p else None, plens if p else None,
+                                        q_len, rows, dim ** -0.5, dtype)
+        ref.check(out, want, tol, f"prompt {p}")
+    out = att(qd, cache, td, i32([0] * R, dev), prompt_table=pd, prompt_lens=i32([-4] * batch, dev))
+    assert torch.equal(out, torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cross_attention_of_a_handle_much_wider_than_its_calls(dev, dtype):
+    """One handle, from one row and key to its limits, strided queries, in any order."""
+    import beam_search_step_amd as bs
+    B, hq, hk, d = 2, 4, 2, 64
+    att = bs.CrossAttention(B, 300, hq, hk, d, 3000, dtype)
+    for rows, keys in ((300, 3000), (1, 1), (7, 0), (0, 5), (9, 3000), (300, 3), (1, 3000)):
+        g = torch.Generator().manual_seed(rows + keys)
+        wide = torch.randn((B, rows, 3 * hq, d), generator=g).to(DT[dtype])
+        k, v = [torch.randn((B, keys, hk, d), generator=g).to(DT[dtype]) for _ in range(2)]
+        say("wide handle", rows, keys, dtype)
+        out = att(wide.to(dev)[:, :, hq:2 * hq], k.to(dev), v.to(dev))
+        assert out.shape == (B, rows, hq, d)
+        want, tol = cross_want(wide[:, :, hq:2 * hq].double(), k.double(), v.double(), None, None, d ** -0.5, dtype)
+        if rows:
+            ref.check(out, want, tol, f"{rows} rows, {keys} keys")
