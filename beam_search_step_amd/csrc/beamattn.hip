@@ -288,11 +288,13 @@ void launch_cross(const CrossArgs& a, int dtype, int nm, int nw, dim3 grid, hipS
   }
 }
 
-// bf16: more columns than this share keys through LDS, of 14 items of 8 kv heads and
-// 1403 keys: 56 columns of 64 values 26 us against 40, 32 columns 25 against 20; 56
-// of 128 values 35 against 61, 32 columns of 96 29 against 37; 56 of 256 values 88
-// against 118, 24 columns 80 against 78.
-int tile_cols(int dp) { return dp == 128 ? 16 : 32; }
+// bf16: more columns than this share keys through LDS (a3_tile). Of 14 items, 8 kv heads
+// and 1403 keys, with the launch that joins split sums where there is one, streamed and
+// tiled: 64 values 64 columns 24 and 25 us, 80 columns 27 and 26, 128 columns 32 and 28; 128
+// values 32 columns 33 and 34, 40 columns 39 and 35; 256 values 40 columns 76 and 81, 56
+// columns 92 and 85. Of 64 items and 600 keys: 64 values 64 columns 31 and 41, 128 columns
+// 49 and 34; 128 values 32 columns 62 and 59, 64 columns 99 and 68.
+int tile_cols(int dp) { return dp == 64 ? 64 : dp == 128 ? 32 : 48; }
 // Waves of 32 columns in its workgroup. Eight, which bring a tile in for twice the
 // columns, where they are a workgroup for every CU at least (the rate at 32 heads of
 // 128 is 320 us against 333); heads of 256 leave registers for four.
