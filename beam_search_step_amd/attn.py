@@ -166,13 +166,12 @@ def _check_stream(stream, device) -> None:
         raise ValueError(f"stream: on {stream.device}, expected {device}")
 
 
-def _record_use(obj, *tensors) -> None:
-    """Before a call of an object without a stream: under another stream than the one it was
-    made under, tells the allocator that its memory is used there too."""
+def _record_use(device, *tensors) -> None:
+    """Tells the allocator that an object's memory is used on the current stream too, where
+    that is another than the one it was made under."""
     torch = _t()
-    if torch._C._cuda_getCurrentRawStream(obj.device.index) != obj._raw and \
-            not torch.cuda.is_current_stream_capturing():
-        now = torch.cuda.current_stream(obj.device)
+    if not torch.cuda.is_current_stream_capturing():
+        now = torch.cuda.current_stream(device)
         for t in tensors:
             t.record_stream(now)
 
@@ -265,7 +264,8 @@ class BlockMap:
         self._cu, self._used = self.cu.data_ptr(), self.used.data_ptr()
         self._slots = self.slots.data_ptr() or None
         self._table = None
-        self._raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        self._current = torch._C._cuda_getCurrentRawStream
+        self._raw = self._current(self.device.index)
 
     def __call__(self, lens, free_blocks=None, starts=None, table=None):
         torch = _t()
@@ -293,8 +293,8 @@ class BlockMap:
         at, width = _table_arg(table, self.n, dev, self.block_size)
         if width != self.max_blocks:
             raise ValueError(f"table: {width} entries per row, expected {self.max_blocks}")
-        if self.stream is None:
-            _record_use(self, self.cu, self.slots, self.used,
+        if self.stream is None and self._current(dev.index) != self._raw:
+            _record_use(dev, self.cu, self.slots, self.used,
                         *(() if self._table is None else (self._table,)))
         # an empty list is a list still: any address will do
         free = None if free_blocks is None else free_blocks.data_ptr() or self._used
@@ -343,7 +343,8 @@ class QuantCache:
                                 v_scale.data_ptr(), n, bs, h, d, block, pos)
         self._ref = ctypes.addressof(self.desc)
         self._dtypes = _torch_dtypes()
-        self._raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        self._current = torch._C._cuda_getCurrentRawStream
+        self._raw = self._current(self.device.index)
         self._write, self._read = attn_library().bs_kvq_write, attn_library().bs_kvq_read
 
     @classmethod
@@ -371,8 +372,8 @@ class QuantCache:
         if slots.dim() != 1 or slots.shape[0] < n or n > _MOST or not slots.is_contiguous():
             raise ValueError(f"slots: a contiguous list of at least {n} (and {n} at most {_MOST}) "
                              "is needed")
-        if self.stream is None:
-            _record_use(self, self.k, self.v, self.k_scale, self.v_scale)
+        if self.stream is None and self._current(self.device.index) != self._raw:
+            _record_use(self.device, self.k, self.v, self.k_scale, self.v_scale)
         _bs._check(_on_device(self.device, self.stream, self._write, self._ref,
                               _bs.BS_F32 if f32 else _bs.BS_BF16, k.data_ptr(), v.data_ptr(),
                               stride, slots.data_ptr(), n), "bs_kvq_write")
@@ -390,8 +391,8 @@ class QuantCache:
             with torch.cuda.stream(self.stream):
                 kv = torch.empty(shape, dtype=self._dtypes[dtype], device=self.device)
         k, v = kv.unbind(0)
-        if self.stream is None:
-            _record_use(self, self.k, self.v, self.k_scale, self.v_scale)
+        if self.stream is None and self._current(self.device.index) != self._raw:
+            _record_use(self.device, self.k, self.v, self.k_scale, self.v_scale)
         _bs._check(_on_device(self.device, self.stream, self._read, self._ref, _bs.DTYPES[dtype],
                               slots.data_ptr(), n, k.data_ptr(), v.data_ptr()), "bs_kvq_read")
         return k, v

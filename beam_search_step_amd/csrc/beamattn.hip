@@ -141,8 +141,7 @@ int choose_splits(int64_t groups, int64_t keys, int most) {
   int64_t s = (kWantGroups + groups - 1) / groups;
   // chunks of more than 2048 keys: a third more of them, so that the last
   // workgroups of ragged lengths are not late (8 prompts of 16,000 to 48,000
-  // tokens: 124 us against 131; 1500-key sources are 22 us with three chunks, 25
-  // with four)
+  // tokens: 131 us and 6 of the joining launch, against 134 and 5)
   if (keys > 2048 * s) s = (kWantGroups + kWantGroups / 3 + groups - 1) / groups;
   const int64_t by_keys = (keys + kMinKeys - 1) / kMinKeys;
   if (s > by_keys) s = by_keys;
@@ -152,10 +151,11 @@ int choose_splits(int64_t groups, int64_t keys, int most) {
 
 // Waves of a workgroup, for the kernels of one column tile. One where units are
 // short and so many that a wave each fills the device (the wide search's 16 beams
-// of 16 heads over 128 positions: 30 us, with four waves 34). Eight where there are
+// of 16 heads over 128 positions: 31 us, with four waves 34). Eight where there are
 // units enough to go without partial sums and the launch that joins them: 64
-// sequences of 8 heads and 500 keys, 15.8 us against 20; 1000-key fp32 sources of
-// 16 by 16 heads, 38 against 40. Four else.
+// sequences of 8 heads and 500 keys, 16.0 us against 19.7; 1000-key fp32 sources of
+// 16 by 16 heads, 39.7 against 40.2, 1500-key bf16 ones 26.5 against 26.4. Four else.
+// Measured up to 2000 keys: far longer ragged ones would wait for their last workgroup.
 int choose_waves(int64_t pairs, int64_t keys, bool one_kind) {
   if (pairs >= 2048 && keys <= 512) return 1;
   return one_kind && pairs >= 256 && keys > 256 ? 8 : 4;
@@ -165,15 +165,15 @@ int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 // The most 16-column tiles of a wave of a2_cross. Two where keys are worth reading
 // once for both and registers hold them without spilling: 32 columns of 14 items, 8 kv
-// heads of 64 and 1403 bf16 keys are 19 us, one tile at a time 23; 4096 columns of 512
-// fp32 keys 388 us against 575 and with four tiles 461.
+// heads of 64 and 1403 bf16 keys are 15.1 us, one tile at a time 16.4; 4096 columns of 2
+// items, 8 kv heads of 64 and 512 fp32 keys 108 us against 151.
 template <int DP, typename T>
 constexpr int cross_most() {
   return sizeof(T) == 2 ? (DP == 64 ? 2 : 1) : DP <= 128 ? 2 : 1;
 }
-// The tiles of a call, never more than that. fp32 heads of 128: 56 columns of 1403 keys
-// are 93 us one tile at a time (two: 116 where groups were dealt over the XCDs, one
-// 110), 4096 columns of 512 keys 1170 and 1006
+// The tiles of a call, never more than that. fp32 heads of 128: 56 columns of 14 items
+// and 1403 keys are 88 us one tile at a time and 119 with two, 4096 columns of 2 items and
+// 512 keys 295 and 237
 int cross_tiles(int64_t cols, int dp, int dtype) {
   if (cols <= 16 || (dtype == BS_F32 && dp == 128 && cols <= 64)) return 1;
   if (dtype == BS_F32)
@@ -290,14 +290,14 @@ void launch_cross(const CrossArgs& a, int dtype, int nm, int nw, dim3 grid, hipS
 
 // bf16: more columns than this share keys through LDS (a3_tile). Of 14 items, 8 kv heads
 // and 1403 keys, with the launch that joins split sums where there is one, streamed and
-// tiled: 64 values 64 columns 24 and 25 us, 80 columns 27 and 26, 128 columns 32 and 28; 128
-// values 32 columns 33 and 34, 40 columns 39 and 35; 256 values 40 columns 76 and 81, 56
-// columns 92 and 85. Of 64 items and 600 keys: 64 values 64 columns 31 and 41, 128 columns
-// 49 and 34; 128 values 32 columns 62 and 59, 64 columns 99 and 68.
+// tiled: 64 values 64 columns 24 and 25 us, 80 columns 27 and 26, 128 columns 32 and 29; 128
+// values 32 columns 33 and 34, 40 columns 40 and 35; 256 values 40 columns 76 and 80, 56
+// columns 93 and 85. Of 64 items and 600 keys: 64 values 64 columns 31 and 41, 128 columns
+// 50 and 34; 128 values 32 columns 63 and 59, 64 columns 99 and 67.
 int tile_cols(int dp) { return dp == 64 ? 64 : dp == 128 ? 32 : 48; }
 // Waves of 32 columns in its workgroup. Eight, which bring a tile in for twice the
-// columns, where they are a workgroup for every CU at least (the rate at 32 heads of
-// 128 is 320 us against 333); heads of 256 leave registers for four.
+// columns, where they are a workgroup for every CU at least (8 x 1024 rows over 2048
+// keys, 32 heads of 128: 431 us against 448); heads of 256 leave registers for four.
 int tile_waves(int64_t pairs, int64_t cols, int dp) {
   return dp <= 128 && cols > 128 && pairs * ((cols + 255) / 256) >= 256 ? 8 : 4;
 }

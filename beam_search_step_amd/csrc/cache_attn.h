@@ -185,19 +185,18 @@ __device__ __forceinline__ void widen_v(const RawKv<DP>& x, bf16x8 (&vf)[DP / 16
   gather_v<VD>(rows, vf);
 }
 
-// Prompts of 16,000 to 48,000 tokens for 8 items of 4 beams, 32 heads on 8 of 128: 126
-// us, 4.3 TB/s, bound by memory (a head whose bytes are 384 mod 1024 takes a third
-// longer than the others); of 1000 tokens: 12.5, bound by the launch and the chain of
+// Prompts of 16,000 to 48,000 tokens for 8 items of 4 beams, 32 heads on 8 of 128: 131
+// us, 4.1 TB/s, bound by memory (a head whose bytes are 384 mod 1024 takes a third
+// longer than the others); of 1000 tokens: 12.7, bound by the launch and the chain of
 // lengths, table and keys.
 // 16 columns a wave: two or four tiles of them read a key once for all, but leave no
 // registers for a second wave (16 items, 16 beams of 4 heads a kv head, prompts of
-// 1000 tokens: 27 us at 64 values a head, with two tiles 38, with four 75; 45 at 128,
-// with two 85).
+// 1000 tokens: 20 us at 64 values a head, with two tiles 30; 33 at 128, with two 66).
 // Waves a SIMD that the registers have to leave, as many as go without spilling:
 // left to itself the compiler keeps sums in a second register file and one wave
 // fewer (16 beams of 4 heads a kv head over prompts of 1000 tokens, 256 values a
-// head: two waves 72 us, one 118; 128 fp32 values: three 51, two 67; the wide
-// search's 4352 one-wave workgroups: five, all resident, 30, four 32).
+// head: two waves 60 us, one 104; 128 fp32 values: three 45, two 59; the wide
+// search's 4352 one-wave workgroups: five, all resident, 31, four 32).
 template <int DP, int NW, int NT, bool UNI>
 constexpr int cache_waves() {
   return DP == 64 ? (NT == 1 || NW == 1 ? 5 : 4)

@@ -221,7 +221,7 @@ __device__ __forceinline__ void step_f32(const QueryF32<DP, NM>& q, Softmax<NM>&
 // Workgroup idx of `units` x `groups`: the column groups of a unit read the same
 // keys, so they follow each other on one XCD, whose L2 then holds them. Workgroups
 // go round the eight XCDs; units past the last eight are dealt as they come. 56 fp32
-// columns of 1403 keys, heads of 128: 93 us against 111. (Over the cache, whose keys are
+// columns of 1403 keys, heads of 128: 88 us against 108. (Over the cache, whose keys are
 // a quarter as wide, it measured nothing.)
 __device__ __forceinline__ void unit_and_group(int idx, int units, int groups, int& unit,
                                                int& group) {
@@ -242,9 +242,9 @@ __device__ __forceinline__ void unit_and_group(int idx, int units, int groups, i
 }
 
 // Bound by bandwidth where keys are many and columns few: 16 items of 16 heads of 64,
-// 1500 bf16 keys, 26.7 us, 3.7 TB/s; 1000 fp32 keys 38.7, 3.4 TB/s.
+// 1500 bf16 keys, 26.5 us, 3.7 TB/s; 1000 fp32 keys 39.7, 3.4 TB/s.
 // Waves a SIMD that the registers have to leave (fp32 heads of 128, 48 items of 2
-// heads and 4829 keys: two 122 us, one 145).
+// heads, 4 rows and 4829 keys: two 108 us, one 120).
 template <int DP, int NM, typename T>
 constexpr int cross_waves() {
   return sizeof(T) == 4 ? (NM == 1 && DP == 128 ? 2 : 1)

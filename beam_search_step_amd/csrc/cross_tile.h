@@ -19,15 +19,15 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 //                 register 4 b + r is value 32 j + 8 b + 4 hh + r
 // The next tile's loads go straight to LDS while this one is used, so they take no
 // registers, no instructions to turn V, and no writes. 8 items of 1024 rows over
-// 2048 keys, 32 heads of 128: 390 us, 705 TFLOP/s, or 1060 of matrix instructions, the
+// 2048 keys, 32 heads of 128: 431 us, 640 TFLOP/s, or 960 of matrix instructions, the
 // second product being done in two terms. In one term (2^-8 of a probability instead
-// of 2^-15) it is 293 us, but a query would then be answered less exactly beside many
+// of 2^-15) it is 320 us, but a query would then be answered less exactly beside many
 // rows than beside few, where the other kernels keep two. Between two barriers the
 // waves meet at the loads (32 KB at the 64 bytes a cycle that a CU takes in), the
 // exponentials, and the barrier. Tried and no better: each 16 keys' exponentials right
-// before their products, both terms' products side by side over the values' tiles;
-// with one term, scores of the next tile during this one's exponentials, two tiles
-// between barriers, priorities for the matrix phases.
+// before their products, one term's products over all values before the other's; with one
+// term, scores of the next tile during this one's exponentials, two tiles between
+// barriers, priorities for the matrix phases.
 template <int DP>
 struct TileLds {
   static constexpr int KT = 8192 / DP;   // keys of a tile: 16 KB of K and of V
