@@ -132,10 +132,12 @@ int bs_kvq_reorder(bs_kv_paged *p, const bs_kvq_desc *layers, int32_t n_layers, 
  * the first lens[r] - (q_len - 1) + i of the row's own positions (the last
  * q_len of them are the queries' own, each seeing those before it), and
  *   out = sum_j softmax_j(scale * q . k_j) v_j
- * in fp32 arithmetic, rounded once. A position whose table entry is not a
- * block of the cache (-1, out of range) is not seen. A query that sees nothing,
- * or whose scores are all -inf, gives zeros. Positions past the lengths may
- * hold anything, NaN included. */
+ * in fp32 arithmetic, rounded once (the probabilities of bf16 outputs are held
+ * to 2^-15). A position whose table entry is not a block of the cache (-1, out
+ * of range) is not seen. A query that sees nothing, or whose scores are all
+ * -inf, gives zeros, whatever the values hold. Positions past the lengths may
+ * hold anything, NaN included, and so may the scales of blocks without a seen
+ * position. */
 typedef struct {
     int32_t batch;             /* B >= 1                                        */
     int32_t rows;              /* rows of an item (beams), >= 1;
@@ -182,9 +184,10 @@ void bs_cache_attn_destroy(bs_cache_attn_state *h);
 /* Attention of an item's rows (its beams, a verify's positions, or a whole
  * target) to its encoder's states, all of them seeing the same keys:
  * out = sum_j softmax_j(scale * q . k_j) v_j over j < lens[b] with
- * mask[b][j] != 0, in fp32 arithmetic, rounded once. Query head h uses kv head
- * h / (heads / kv_heads). An item that sees nothing, or a query whose scores
- * are all -inf, gives zeros. Keys past the length are not read; keys and values
+ * mask[b][j] != 0, in fp32 arithmetic, rounded once (the probabilities of bf16
+ * calls are held to 2^-15, however many rows share a call). Query head h uses kv
+ * head h / (heads / kv_heads). An item that sees nothing, or a query whose scores
+ * are all -inf, gives zeros, whatever the values hold. Keys past the length are not read; keys and values
  * under a zero of the mask may hold anything, NaN included. */
 typedef struct {
     int32_t batch;     /* B >= 1                                                */
