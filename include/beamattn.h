@@ -187,8 +187,9 @@ void bs_cache_attn_destroy(bs_cache_attn_state *h);
  * mask[b][j] != 0, in fp32 arithmetic, rounded once (the probabilities of bf16
  * calls are held to 2^-15, however many rows share a call). Query head h uses kv
  * head h / (heads / kv_heads). An item that sees nothing, or a query whose scores
- * are all -inf, gives zeros, whatever the values hold. Keys past the length are not read; keys and values
- * under a zero of the mask may hold anything, NaN included. */
+ * are all -inf, gives zeros, whatever the values hold. Keys past the length are
+ * not read; keys and values under a zero of the mask may hold anything, NaN
+ * included. */
 typedef struct {
     int32_t batch;     /* B >= 1                                                */
     int32_t max_rows;  /* the most query rows of an item, >= 1                  */
